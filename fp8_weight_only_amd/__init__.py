@@ -27,7 +27,11 @@ import os
 
 import torch
 
+from . import moe
+from .moe import *  # noqa: F401,F403  (routing, products grouped by expert, the int8 layer)
+
 __all__ = [
+    *moe.__all__,
     "Fp8wError", "lib_path", "load", "fp8w_quantize", "fp8w_linear", "fp8w_linear_with_path", "fp8w_linear_noalloc", "linear_noalloc", "SCRATCH_BYTES",
     "fp8w_dequantize_fallback", "fp8w_linear_path", "fp8w_linear_workspace_bytes", "fp8w_linear_with_path_workspace_bytes",
     "fp8w_linear_kernel",

@@ -1,7 +1,9 @@
-"""Build libfp8w.so (the HIP kernels + C ABI) in-tree for gfx950 with hipcc.
+"""Build libfp8w.so and libfp8w_moe.so (the HIP kernels + C ABIs) in-tree for gfx950 with hipcc.
 
 Every source under csrc/ is compiled to an object in parallel, then linked into
-``fp8_weight_only_amd/libfp8w.so``. Flags: -O3, IEEE fp32 division (no
+``fp8_weight_only_amd/libfp8w.so`` (the FP8 linear layer, include/fp8w.h); those
+under csrc/moe/ go into ``fp8_weight_only_amd/libfp8w_moe.so`` (routing, products
+grouped by expert, the int8 layer, include/fp8w_moe.h). Flags: -O3, IEEE fp32 division (no
 fast-math), hidden visibility except the C ABI, packed-fp32 instructions
 disabled (the compiler's own choice of v_pk_*_f32 is switched off), and kernel
 arguments preloaded into SGPRs at wave launch (up to 16 SGPRs' worth). With
@@ -22,6 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8w.so")
+MOE_LIB = os.path.join(HERE, "libfp8w_moe.so")
 OBJDIR = os.path.join(ROOT, "_build", "fp8w")
 ARCH = os.environ.get("FP8W_ARCH", "gfx950")
 
@@ -45,8 +48,12 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
+def moe_sources():
+    return sorted(glob.glob(os.path.join(CSRC, "moe", "*.hip")))
+
+
 def _compile(src: str, verbose: bool) -> str:
-    obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
+    obj = os.path.join(OBJDIR, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
     cmd = [_hipcc(), *CFLAGS, "-c", src, "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -60,17 +67,23 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(OBJDIR, exist_ok=True)
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-    tmp = LIB + ".tmp"
+def _link(objs, lib: str, verbose: bool) -> None:
+    tmp = lib + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.replace(tmp, lib)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(OBJDIR, exist_ok=True)
+    libs = [(LIB, sources()), (MOE_LIB, moe_sources())]
+    srcs = [s for _, part in libs for s in part]
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
+    for lib, part in libs:
+        _link([objs[s] for s in part], lib, verbose)
     return LIB
 
 
