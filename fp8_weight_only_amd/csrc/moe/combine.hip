@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
         pk.y = (uint32_t)o[2] | ((uint32_t)o[3] << 16);
         pk.z = (uint32_t)o[4] | ((uint32_t)o[5] << 16);
         pk.w = (uint32_t)o[6] | ((uint32_t)o[7] << 16);
-        reinterpret_cast<Any16*>(dst)->v = pk;
+        store16_any(dst, pk);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)

@@ -10,13 +10,16 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes at any address (the hardware takes unaligned global accesses).
-struct __attribute__((packed, aligned(1))) Any16 {
-    u32x4 v;
-};
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 
 __device__ __forceinline__ u32x4 load16_any(const void* p)
 {
-    return static_cast<const Any16*>(p)->v;
+    return *static_cast<const u32x4_any*>(p);
+}
+
+__device__ __forceinline__ void store16_any(void* p, u32x4 v)
+{
+    *static_cast<u32x4_any*>(p) = v;
 }
 
 // The first `avail` of 16 bytes at p, zeros after them; reads no byte past them.
