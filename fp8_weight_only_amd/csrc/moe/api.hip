@@ -281,7 +281,7 @@ fp8w_status_t fp8w_gemm_int8(const int8_t* qx, const float* sx, int64_t m, int64
     if (overlaps_any({y, (size_t)m * (size_t)n * 2}, in))
         return FP8W_ERR_INVALID_VALUE;
     return hip_status(
-        fp8w::launch_gemm_int8(qx, k, sx, m, k, q, scale, bias, n, y, act_of(out_dtype), stream));
+        fp8w::launch_gemm_int8(qx, sx, m, k, q, scale, bias, n, y, act_of(out_dtype), stream));
 }
 
 size_t fp8w_linear_int8_workspace_bytes(int64_t m, int64_t n, int64_t k, const void* x, const int8_t* q)

@@ -11,6 +11,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // 16 bytes at any address (the hardware takes unaligned global accesses).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 
 __device__ __forceinline__ u32x4 load16_any(const void* p)
 {
@@ -35,6 +36,20 @@ __device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t avail)
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
+// The largest v of the wave, in every lane: DPP shifts within rows of 16 lanes,
+// row maxima broadcast upwards, lane 63's result read back.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+{
+    auto step = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));  // row_shr:1
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));  // row_shr:2
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));  // row_shr:4
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));  // row_shr:8
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));  // row_bcast:15
+    v = step(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 template <typename A>
 struct is_bf16 {
     static constexpr bool value = false;
@@ -55,21 +70,34 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
                                                       0, 0, 0);
 }
 
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int v)
+{
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+__device__ __forceinline__ const uint8_t* uniform(const void* p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+}
+
 // Tile (tn, tm) of linear workgroup id L < TN * TM. Workgroups are dealt to the
 // 8 XCDs in turn; each XCD is given a contiguous range of tile ids, walked in
 // groups of GM row tiles, so the tiles that one XCD holds at a time share
 // operand rows in its L2.
 template <int GM>
-__device__ __forceinline__ void xcd_tile(int64_t L, int64_t TN, int64_t TM, int64_t& tn, int64_t& tm)
+__device__ __forceinline__ void xcd_tile(int L, int TN, int TM, int& tn, int& tm)
 {
-    const int64_t T = TN * TM;
-    const int64_t xcd = L % 8, loc = L / 8, q = T / 8, r = T % 8;
-    const int64_t id = xcd * q + (xcd < r ? xcd : r) + loc;
-    const int64_t grp = id / (GM * TN), first = grp * GM;
-    const int64_t gs = TM - first < GM ? TM - first : GM;
-    const int64_t w = id - grp * GM * TN;
-    tm = first + w % gs;
-    tn = w / gs;
+    const int T = TN * TM;  // fewer than 2^24 (a launch has fewer than 2^32 threads)
+    const int xcd = L % 8, loc = L / 8, q = T / 8, r = T % 8;
+    const int id = xcd * q + (xcd < r ? xcd : r) + loc;
+    const int grp = id / (GM * TN), first = grp * GM;
+    const int gs = TM - first < GM ? TM - first : GM;
+    const int w = id - grp * GM * TN;
+    tm = uniform(first + w % gs);
+    tn = uniform(w / gs);
 }
 
 // Four consecutive channels of one token: one 8-byte store where it is aligned

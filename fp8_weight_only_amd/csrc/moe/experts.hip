@@ -166,23 +166,22 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
 // 64 k pass through registers (the next stage's loads are in flight during this
 // one's products) into LDS, the codes decoded on the way.
 template <typename A>
-__global__ __launch_bounds__(256) void experts_any_kernel(ExpertCall c, int64_t TN)
+__global__ __launch_bounds__(256) void experts_any_kernel(ExpertCall c, int TN)
 {
     constexpr int BN = 64, BM = 64, LD = 72;  // LD: row pitch in elements; 16-byte reads of 16 rows spread over banks
     __shared__ __attribute__((aligned(16))) uint16_t sw[2][BN * LD];
     __shared__ __attribute__((aligned(16))) uint16_t sx[2][BM * LD];
-    int64_t tn = 0;
-    const int64_t L = blockIdx.x;
+    const int L = blockIdx.x;
     TileFinder<BM> finder(c.offsets, (int)c.e, (int)c.m);
     const int total = finder.total();
     if (L >= TN * total)
         return;
-    int64_t tm;
+    int tn, tm;
     xcd_tile<4>(L, TN, total, tn, tm);
-    const RowTile tile = finder.find((int)tm);
+    const RowTile tile = finder.find(tm);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int i = lane & 31, h = lane >> 5, wn = wave & 1, wm = wave >> 1;
-    const int64_t n0 = tn * BN;
+    const int64_t n0 = (int64_t)tn * BN;
     f32x16 acc = f32x16{0.0f};
     if (tile.expert < (int)c.e) {
         // this thread's 16 codes of one weight row and 8 values of two rows of x in each stage
@@ -297,7 +296,7 @@ hipError_t launch_typed(const ExpertCall& c, hipStream_t stream)
                            : launch_stream<A, 1, 4>(c, stream);
     }
     const int64_t TN = (c.n + 63) / 64, groups = TN * max_row_tiles(c.m, c.e, 64);
-    hipLaunchKernelGGL(experts_any_kernel<A>, dim3((unsigned)groups), dim3(256), 0, stream, c, TN);
+    hipLaunchKernelGGL(experts_any_kernel<A>, dim3((unsigned)groups), dim3(256), 0, stream, c, (int)TN);
     return hipGetLastError();
 }
 

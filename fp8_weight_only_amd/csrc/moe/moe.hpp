@@ -68,7 +68,7 @@ const char* experts_kernel_name(int64_t m, int64_t e, int64_t n, int64_t k, cons
 hipError_t launch_quantize_int8(const void* x, Act type, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale,
                                 hipStream_t stream);
 // qx [m, k] dense.
-hipError_t launch_gemm_int8(const int8_t* qx, int64_t kx, const float* sx, int64_t m, int64_t k, const int8_t* qw,
+hipError_t launch_gemm_int8(const int8_t* qx, const float* sx, int64_t m, int64_t k, const int8_t* qw,
                             const float* sw, const void* bias, int64_t n, void* y, Act out, hipStream_t stream);
 size_t linear_int8_workspace_bytes(int64_t m, int64_t n, int64_t k, const void* x, const int8_t* q);
 hipError_t launch_linear_int8(const void* x, Act act, int64_t m, int64_t k, const int8_t* qw, const float* sw,

@@ -62,16 +62,6 @@ __device__ __forceinline__ float logit_of(uint32_t key)
     return __builtin_bit_cast(float, (key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
-{
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        const uint32_t o = __shfl_xor(v, off, kWave);
-        v = v > o ? v : o;
-    }
-    return v;
-}
-
 // J registers of logits per lane: e <= 64 J.
 template <int J>
 __device__ __forceinline__ void choose(const void* logits, Act type, int64_t t, int e, int top, bool renorm,
