@@ -15,6 +15,7 @@
 #include "device.hpp"
 #include "groups.hpp"
 #include "moe.hpp"
+#include "tile.hpp"
 
 namespace fp8w {
 namespace {
@@ -162,100 +163,454 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
     }
 }
 
-// Any k, any alignment: 64 channels x 64 rows, four waves of 32 x 32. Stages of
-// 64 k pass through registers (the next stage's loads are in flight during this
-// one's products) into LDS, the codes decoded on the way.
-template <typename A>
-__global__ __launch_bounds__(256) void experts_any_kernel(ExpertCall c, int TN)
-{
-    constexpr int BN = 64, BM = 64, LD = 72;  // LD: row pitch in elements; 16-byte reads of 16 rows spread over banks
-    __shared__ __attribute__((aligned(16))) uint16_t sw[2][BN * LD];
-    __shared__ __attribute__((aligned(16))) uint16_t sx[2][BM * LD];
-    const int L = blockIdx.x;
-    TileFinder<BM> finder(c.offsets, (int)c.e, (int)c.m);
-    const int total = finder.total();
-    if (L >= TN * total)
-        return;
-    int tn, tm;
-    xcd_tile<4>(L, TN, total, tn, tm);
-    const RowTile tile = finder.find(tm);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int i = lane & 31, h = lane >> 5, wn = wave & 1, wm = wave >> 1;
-    const int64_t n0 = (int64_t)tn * BN;
-    f32x16 acc = f32x16{0.0f};
-    if (tile.expert < (int)c.e) {
-        // this thread's 16 codes of one weight row and 8 values of two rows of x in each stage
-        const int64_t wrow = n0 + (tid >> 2);
-        const uint8_t* wp = c.q + ((int64_t)tile.expert * c.n + (wrow < c.n ? wrow : 0)) * c.k + 16 * (tid & 3);
-        const bool won = wrow < c.n;
-        const uint8_t* xp[2];
-        bool xon[2];
+// ------------------------------------------------------------------ tiles
+// More rows per expert: BN channels x BM rows of one expert, WN x WM waves of
+// 32 x 32 fragments, stages of 64 k. In LDS a stage holds BN rows of 64 codes,
+// their four 16-byte chunks rotated by row / 4, and BM rows of 64 activations,
+// their eight chunks rotated by row / 2, so the 16 lanes of a read's phase (16
+// rows, same chunk) hit distinct banks. The codes are decoded on their way from
+// LDS to the matrix cores: every e4m3 value is a bf16 and an fp16 value.
+//
+// A half of a stage is 32 k: lane (i, h) takes the 16 codes and the 16 values at
+// k = 16 h of its rows, eight for each of two v_mfma_f32_32x32x16. Which k meet
+// in one instruction does not matter as long as both operands agree.
+template <typename A, int BN, int BM, int WN, int WM>
+struct ExpertTile {
+    static constexpr int W = WN * WM, NT = W * kWave, FN = BN / WN / 32, FM = BM / WM / 32;
+    static constexpr int ABYTES = BN * 64, STAGE = ABYTES + BM * 128;
+    static_assert(BN == FN * WN * 32 && BM == FM * WM * 32, "tile and wave layout");
+    struct Frags {
+        u32x4 a[FN], x[FM][2];
+    };
+    int lane, wave, wn, wm;
+
+    __device__ __forceinline__ void read(const uint8_t* buf, int j, Frags& f) const
+    {
+        const int i = lane & 31, h = lane >> 5;
+        // one addition to the buffer's address per read: through longer chains the compiler
+        // loses which buffer is read, and waits for every load in flight
+        const int oa = 64 * (wn * (BN / WN) + i) + 16 * ((2 * j + h + (i >> 2)) & 3);
+        const int ox = ABYTES + 128 * (wm * (BM / WM) + i);
+        const int o0 = ox + 16 * ((4 * j + 2 * h + (i >> 1)) & 7), o1 = ox + 16 * ((4 * j + 2 * h + 1 + (i >> 1)) & 7);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = (tid >> 3) + 32 * u;
-            int64_t src = tile.row + r;
-            xon[u] = r < tile.rows;
-            if (xon[u] && c.x_rows)
-                src = c.x_rows[src];
-            xon[u] = xon[u] && src >= 0 && src < c.xr;
-            xp[u] = static_cast<const uint8_t*>(c.x) + 2 * ((xon[u] ? src : 0) * c.k + 8 * (tid & 7));
-        }
-        u32x4 wv, xv[2];
-        auto load = [&](int64_t kb) {
-            wv = load16_part(wp + kb, won ? c.k - kb - 16 * (tid & 3) : 0);
+        for (int q = 0; q < FN; ++q)
+            f.a[q] = *reinterpret_cast<const u32x4*>(buf + (oa + 2048 * q));
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                xv[u] = load16_part(xp[u] + 2 * kb, xon[u] ? 2 * (c.k - kb - 8 * (tid & 7)) : 0);
-        };
-        auto put = [&](int b) {
-            const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
-            uint16_t* d = &sw[b][(tid >> 2) * LD + 16 * (tid & 3)];
+        for (int q = 0; q < FM; ++q)
+            f.x[q][0] = *reinterpret_cast<const u32x4*>(buf + (o0 + 4096 * q));
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const u32x2 p0 = A::decode4(w4[2 * v]), p1 = A::decode4(w4[2 * v + 1]);
-                *reinterpret_cast<u32x4*>(d + 8 * v) = u32x4{p0.x, p0.y, p1.x, p1.y};
+        for (int q = 0; q < FM; ++q)
+            f.x[q][1] = *reinterpret_cast<const u32x4*>(buf + (o1 + 4096 * q));
+    }
+
+    __device__ __forceinline__ void mma(const Frags& f, f32x16* acc) const
+    {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            u32x4 a[FN];
+#pragma unroll
+            for (int q = 0; q < FN; ++q) {
+                const u32x4 v = f.a[q];
+                const u32x2 d0 = A::decode4(t ? v.z : v.x), d1 = A::decode4(t ? v.w : v.y);
+                a[q] = u32x4{d0.x, d0.y, d1.x, d1.y};
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                *reinterpret_cast<u32x4*>(&sx[b][((tid >> 3) + 32 * u) * LD + 8 * (tid & 7)]) = xv[u];
-        };
-        int b = 0;
-        if (c.k > 0) {
-            load(0);
-            put(0);
-        }
-        __syncthreads();
-        for (int64_t kb = 0; kb < c.k; kb += 64, b ^= 1) {
-            const bool more = kb + 64 < c.k;
-            if (more)
-                load(kb + 64);
+            for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(&sw[b][(32 * wn + i) * LD + 16 * j + 8 * h]);
-                const u32x4 bb = *reinterpret_cast<const u32x4*>(&sx[b][(32 * wm + i) * LD + 16 * j + 8 * h]);
-                acc = mfma32<A>(a, bb, acc);
-            }
-            if (more)
-                put(b ^ 1);
-            __syncthreads();
+                for (int fm = 0; fm < FM; ++fm)
+                    acc[fn * FM + fm] = mfma32<A>(a[fn], f.x[fm][t], acc[fn * FM + fm]);
         }
     }
-    // lane (i, h) holds channels 8 j + 4 h + r of row i in accumulators 4 j + r
-    const int rl = 32 * wm + i;
-    if (rl >= tile.rows)
-        return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t c0 = n0 + 32 * wn + 8 * j + 4 * h;
-        const int64_t left = c.n - c0;
-        const float v[4] = {acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]};
-        if (left > 0)
-            store_tile_row<A>(c, tile.row + rl, tile.expert, c0, left < 4 ? (int)left : 4, v);
+};
+
+// What a tile's epilogue needs: the channels' scales and biases, and where each
+// row goes (-1: nowhere) and whether its source exists.
+template <int BN, int BM>
+struct ExpertEpilogue {
+    float scale[BN];
+    uint16_t bias[BN];
+    int dst[BM];
+    bool bad[BM];
+};
+
+// The source row of a tile's row; rows past the tile's and rows that do not
+// exist read some row of x, and are not stored or stored as NaN.
+__device__ __forceinline__ int64_t source_row(const ExpertCall& c, const RowTile& tile, int r)
+{
+    int64_t src = tile.row + (r < tile.rows ? r : 0);
+    if (c.x_rows)
+        src = c.x_rows[src];
+    return src < 0 || src >= c.xr ? 0 : src;
+}
+
+// Fills the epilogue's operands (any thread its share); the caller's barrier
+// stands before their use.
+template <int BN, int BM, int NT>
+__device__ __forceinline__ void fill_epilogue(const ExpertCall& c, const RowTile& tile, int64_t n0,
+                                              ExpertEpilogue<BN, BM>& e)
+{
+    for (int j = threadIdx.x; j < BN; j += NT) {
+        const int64_t ch = n0 + j < c.n ? n0 + j : c.n - 1, at = (int64_t)tile.expert * c.n + ch;
+        const bool on = tile.expert < (int)c.e;
+        e.scale[j] = on ? c.scale[at] : 0.0f;
+        e.bias[j] = on ? bias_bits(static_cast<const uint16_t*>(c.bias), at) : (uint16_t)0;
+    }
+    for (int j = threadIdx.x; j < BM; j += NT) {
+        int dst = -1;
+        bool bad = false;
+        if (j < tile.rows) {
+            const int pos = tile.row + j;
+            dst = c.y_rows ? c.y_rows[pos] : pos;
+            if (dst >= (int)c.m)
+                dst = -1;
+            if (c.x_rows && tile.expert < (int)c.e) {
+                const int src = c.x_rows[pos];
+                bad = src < 0 || src >= c.xr;
+            }
+        }
+        e.dst[j] = dst;
+        e.bad[j] = bad;
     }
 }
 
+// Lane (i, h) holds channels 8 j + 4 h + r of row i in accumulators 4 j + r of
+// each fragment.
+template <typename A, int BN, int BM, int WN, int WM>
+__device__ __forceinline__ void store_tile(const ExpertCall& c, const ExpertTile<A, BN, BM, WN, WM>& p, int64_t n0,
+                                           const ExpertEpilogue<BN, BM>& e, const f32x16* acc)
+{
+    using P = ExpertTile<A, BN, BM, WN, WM>;
+    const int i = p.lane & 31, h = p.lane >> 5;
+#pragma unroll
+    for (int fm = 0; fm < P::FM; ++fm) {
+        const int rl = p.wm * (BM / WM) + 32 * fm + i, dst = e.dst[rl];
+        if (dst < 0)
+            continue;
+        const bool bad = e.bad[rl];
+        uint16_t* out = static_cast<uint16_t*>(c.y) + (int64_t)dst * c.n;
+#pragma unroll
+        for (int fn = 0; fn < P::FN; ++fn)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int cl = p.wn * (BN / WN) + 32 * fn + 8 * j + 4 * h;
+                const int64_t c0 = n0 + cl;
+                const f32x4 s4 = *reinterpret_cast<const f32x4*>(&e.scale[cl]);
+                const u32x2 b4 = *reinterpret_cast<const u32x2*>(&e.bias[cl]);
+                const float bf[4] = {A::lo_f32(b4.x), A::hi_f32(b4.x), A::lo_f32(b4.y), A::hi_f32(b4.y)};
+                uint16_t o[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    o[r] = A::from_f32(bad ? __builtin_nanf("")
+                                           : __builtin_fmaf(s4[r], acc[fn * P::FM + fm][4 * j + r], bf[r]));
+                if (c0 < c.n)
+                    store4(out + c0, o, c.n - c0);
+            }
+    }
+}
+
+// Which tile this workgroup is (false: none).
+template <int BM>
+__device__ __forceinline__ bool find_tile(const ExpertCall& c, int TN, int& tn, RowTile& tile)
+{
+    TileFinder<BM> finder(c.offsets, (int)c.e, (int)c.m);
+    const int total = uniform(finder.total());
+    if ((int)blockIdx.x >= TN * total)
+        return false;
+    int tm;
+    xcd_tile<4>(blockIdx.x, TN, total, tn, tm);
+    tile = finder.find(tm);
+    tile.expert = uniform(tile.expert);
+    tile.row = uniform(tile.row);
+    tile.rows = uniform(tile.rows);
+    return true;
+}
+
+// Any k, any alignment, any number of rows in x: a stage passes through
+// registers into LDS. Stage s + 2 is requested when stage s begins, stage s + 1
+// is written to the other LDS buffer when it ends.
+template <typename A, int BN, int BM, int WN, int WM>
+__global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall c, int TN)
+{
+    using P = ExpertTile<A, BN, BM, WN, WM>;
+    constexpr int LW = BN * 4 / P::NT, LX = BM * 8 / P::NT;
+    static_assert(BN * 4 == LW * P::NT && BM * 8 == LX * P::NT, "chunks split evenly");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][P::STAGE];
+    __shared__ __attribute__((aligned(16))) ExpertEpilogue<BN, BM> epi;
+    int tn;
+    RowTile tile;
+    if (!find_tile<BM>(c, TN, tn, tile))
+        return;
+    const int64_t n0 = (int64_t)tn * BN;
+    const int tid = threadIdx.x;
+    P p;
+    p.lane = tid & 63;
+    p.wave = uniform(tid >> 6);
+    p.wn = p.wave % WN;
+    p.wm = p.wave / WN;
+    fill_epilogue<BN, BM, P::NT>(c, tile, n0, epi);
+    f32x16 acc[P::FN * P::FM];
+#pragma unroll
+    for (int f = 0; f < P::FN * P::FM; ++f)
+        acc[f] = f32x16{0.0f};
+    const int64_t S = tile.expert < (int)c.e && c.xr > 0 ? (c.k + 63) / 64 : 0;
+    if (S > 0) {
+        const uint8_t *wp[LW], *xp[LX];
+        int wo[LW], xo[LX];
+        const int wc = tid & 3, xc = tid & 7;
+#pragma unroll
+        for (int u = 0; u < LW; ++u) {
+            const int r = (tid >> 2) + P::NT / 4 * u;
+            wp[u] = c.q + ((int64_t)tile.expert * c.n + (n0 + r < c.n ? n0 + r : c.n - 1)) * c.k + 16 * wc;
+            wo[u] = 64 * r + 16 * ((wc + (r >> 2)) & 3);
+        }
+#pragma unroll
+        for (int u = 0; u < LX; ++u) {
+            const int r = (tid >> 3) + P::NT / 8 * u;
+            xp[u] = static_cast<const uint8_t*>(c.x) + 2 * (source_row(c, tile, r) * c.k + 8 * xc);
+            xo[u] = P::ABYTES + 128 * r + 16 * ((xc + (r >> 1)) & 7);
+        }
+        struct Regs {
+            u32x4 w[LW], x[LX];
+        };
+        auto load = [&](Regs& g, int64_t s) {
+            const int64_t kb = 64 * s;
+            if (kb + 64 <= c.k) {
+#pragma unroll
+                for (int u = 0; u < LW; ++u)
+                    g.w[u] = load16_any(wp[u] + kb);
+#pragma unroll
+                for (int u = 0; u < LX; ++u)
+                    g.x[u] = load16_any(xp[u] + 2 * kb);
+            } else {
+#pragma unroll
+                for (int u = 0; u < LW; ++u)
+                    g.w[u] = load16_part(wp[u] + kb, c.k - kb - 16 * wc);
+#pragma unroll
+                for (int u = 0; u < LX; ++u)
+                    g.x[u] = load16_part(xp[u] + 2 * kb, 2 * (c.k - kb - 8 * xc));
+            }
+        };
+        auto put = [&](const Regs& g, int b) {
+#pragma unroll
+            for (int u = 0; u < LW; ++u)
+                *reinterpret_cast<u32x4*>(&lds[b][wo[u]]) = g.w[u];
+#pragma unroll
+            for (int u = 0; u < LX; ++u)
+                *reinterpret_cast<u32x4*>(&lds[b][xo[u]]) = g.x[u];
+        };
+        auto compute = [&](int b) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                typename P::Frags f;
+                p.read(lds[b], j, f);
+                p.mma(f, acc);
+            }
+        };
+        Regs r0, r1;
+        load(r0, 0);
+        if (S > 1)
+            load(r1, 1);
+        put(r0, 0);
+        __syncthreads();
+        for (int64_t s = 0; s < S; s += 2) {
+            if (s + 2 < S)
+                load(r0, s + 2);
+            compute(0);
+            if (s + 1 < S)
+                put(r1, 1);
+            __syncthreads();
+            if (s + 1 < S) {
+                if (s + 3 < S)
+                    load(r1, s + 3);
+                compute(1);
+                if (s + 2 < S)
+                    put(r0, 0);
+                __syncthreads();
+            }
+        }
+    } else {
+        __syncthreads();
+    }
+    store_tile(c, p, n0, epi, acc);
+}
+
+// Rows at 16-byte boundaries, k a multiple of 64, x below 2 GiB: the same tiles
+// fed by a ring of NS direct-to-LDS stages (tile.hpp).
+template <typename A, int BN, int BM, int WN, int WM>
+struct ExpertRing : ExpertTile<A, BN, BM, WN, WM> {
+    using T = ExpertTile<A, BN, BM, WN, WM>;
+    static constexpr int LW = BN / 16 / T::W, LX = BM / 8 / T::W, LOADS = LW + LX;  // 1 KB loads per wave and stage
+    static_assert(BN == LW * 16 * T::W && BM == LX * 8 * T::W, "loads split evenly");
+    Rows w, x;
+    int off[LOADS];  // this lane's 16 bytes of each load at k = 0
+    int S, rot;
+
+    __device__ __forceinline__ void issue(int s, uint8_t* buf) const
+    {
+        const int kb = 64 * (s + rot < S ? s + rot : s + rot - S);
+#pragma unroll
+        for (int u = 0; u < LW; ++u)
+            w.load(off[u], kb, buf + 1024 * (u * T::W + this->wave));
+#pragma unroll
+        for (int u = 0; u < LX; ++u)
+            x.load(off[LW + u], 2 * kb, buf + T::ABYTES + 1024 * (u * T::W + this->wave));
+    }
+};
+
+// A wave whose rows all lie past the tile's: it loads its share and keeps the
+// barriers, and leaves the matrix cores to the others.
+template <typename A, int BN, int BM, int WN, int WM>
+struct ExpertRingIdle : ExpertRing<A, BN, BM, WN, WM> {
+    struct Frags {};
+    __device__ __forceinline__ void read(const uint8_t*, int, Frags&) const {}
+    __device__ __forceinline__ void mma(const Frags&, f32x16*) const {}
+};
+
+template <typename A, int BN, int BM, int WN, int WM, int NS>
+__global__ __launch_bounds__(WN* WM* kWave) void experts_ring_kernel(ExpertCall c, int TN)
+{
+    using P = ExpertRing<A, BN, BM, WN, WM>;
+    using T = ExpertTile<A, BN, BM, WN, WM>;
+    static_assert(NS >= 3 && NS <= 8, "stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t b1[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t b2[T::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t b3[NS > 3 ? T::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b4[NS > 4 ? T::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b5[NS > 5 ? T::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b6[NS > 6 ? T::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b7[NS > 7 ? T::STAGE : 16];
+    __shared__ __attribute__((aligned(16))) ExpertEpilogue<BN, BM> epi;
+    auto buf = [&](auto ic) -> uint8_t* {
+        constexpr int i = decltype(ic)::value;
+        if constexpr (i < 4)
+            return ring_buf<i>(b0, b1, b2, b3);
+        else
+            return ring_buf<i - 4>(b4, b5, b6, b7);
+    };
+    int tn;
+    RowTile tile;
+    if (!find_tile<BM>(c, TN, tn, tile))
+        return;
+    const int64_t n0 = (int64_t)tn * BN;
+    const int tid = threadIdx.x;
+    P p;
+    p.lane = tid & 63;
+    p.wave = uniform(tid >> 6);
+    p.wn = p.wave % WN;
+    p.wm = p.wave / WN;
+    f32x16 acc[T::FN * T::FM];
+#pragma unroll
+    for (int f = 0; f < T::FN * T::FM; ++f)
+        acc[f] = f32x16{0.0f};
+    fill_epilogue<BN, BM, T::NT>(c, tile, n0, epi);
+    if (tile.expert < (int)c.e && c.xr > 0) {
+        p.S = (int)(c.k / 64);
+        p.rot = (int)(blockIdx.x % 8) * (p.S / 8);
+        p.w = Rows(c.q + ((int64_t)tile.expert * c.n + n0) * c.k);
+        p.x = Rows(c.x);
+#pragma unroll
+        for (int u = 0; u < P::LW; ++u) {
+            const int r = 16 * (u * T::W + p.wave) + (p.lane >> 2);
+            p.off[u] = (int)((n0 + r < c.n ? r : c.n - 1 - n0) * c.k) + 16 * (((p.lane & 3) - (r >> 2)) & 3);
+        }
+#pragma unroll
+        for (int u = 0; u < P::LX; ++u) {
+            const int r = 8 * (u * T::W + p.wave) + (p.lane >> 3);
+            p.off[P::LW + u] = (int)(2 * source_row(c, tile, r) * c.k) + 16 * (((p.lane & 7) - (r >> 1)) & 7);
+        }
+        if (p.wm * (BM / WM) < tile.rows) {
+            run_tile_ring<NS, P::LOADS>(p, p.S, buf, acc);
+        } else {
+            ExpertRingIdle<A, BN, BM, WN, WM> idle;
+            static_cast<P&>(idle) = p;
+            run_tile_ring<NS, P::LOADS>(idle, p.S, buf, acc);
+        }
+    }
+    __syncthreads();
+    store_tile<A, BN, BM, WN, WM>(c, p, n0, epi, acc);
+}
+
+// ------------------------------------------------------------------ plans
+enum class ExpertKind { STREAM, TILE, RING };
+
+struct ExpertPlan {
+    ExpertKind kind;
+    int a, b, w;  // stream: CT, rows of a tile, W; tile, ring: BN, BM, waves
+    int64_t groups(int64_t m, int64_t e, int64_t n) const
+    {
+        const int64_t bn = kind == ExpertKind::STREAM ? 16 * a : a;
+        return (n + bn - 1) / bn * max_row_tiles(m, e, b);
+    }
+    bool fits(int64_t m, int64_t e, int64_t n) const { return grid_fits(groups(m, e, n), w * kWave); }
+};
+
+constexpr ExpertPlan kRings[] = {{ExpertKind::RING, 256, 256, 8}, {ExpertKind::RING, 256, 128, 8},
+                                 {ExpertKind::RING, 128, 128, 8}, {ExpertKind::RING, 256, 64, 8},
+                                 {ExpertKind::RING, 128, 64, 4},  {ExpertKind::RING, 64, 64, 4},
+                                 {ExpertKind::RING, 256, 32, 4},  {ExpertKind::RING, 128, 32, 4},
+                                 {ExpertKind::RING, 64, 32, 2}};
+constexpr ExpertPlan kTiles[] = {{ExpertKind::TILE, 256, 128, 8}, {ExpertKind::TILE, 128, 64, 4},
+                                 {ExpertKind::TILE, 64, 64, 4}};
+
+// Stages of a ring's tile: what LDS holds.
+constexpr int ring_depth(int bn, int bm)
+{
+    return bn == 256 && bm == 256 ? 3 : 4;
+}
+
+ExpertPlan stream_plan(int64_t active, int64_t n, int64_t k)
+{
+    ExpertPlan p{ExpertKind::STREAM, 4, 16, k >= 2048 ? 8 : 4};
+    while (p.a > 1 && (n + 16 * p.a - 1) / (16 * p.a) * active < 256)
+        p.a /= 2;
+    return p;
+}
+
+// The plan goes by the rows per expert, were they spread evenly over as many
+// experts as can have any (how they are spread only the GPU knows). Measured on
+// [14336, 4096] x 8 and [4096, 1024] x 128 experts, us:
+//   rows per expert     1.6   4     16    32     64     128    256    1024
+//   stream              62    94    127   -      367    -      -      -
+//   256 x 32 (128 x 32) 64    88    89    117    175    366    503    -
+//   256 x 64            -     94    98    103    143    315    374    -
+//   256 x 128           -     -     123   128    129    290    317    980
+//   256 x 256           -     -     -     -      -      344    302    980
+// A tile's channels are halved while it leaves CUs idle; 128 x 32 where k is
+// short (several workgroups per CU then overlap their starts: 85 against 104 us
+// at k = 1024, 4 rows), 256 x 32 where it is long (89 against 96 at k = 4096).
+// Unaligned rows: the stream kernel up to 8 rows, then the tiles.
+ExpertPlan experts_plan(int64_t m, int64_t e, int64_t n, int64_t k, int64_t xr, const void* x, const uint8_t* q)
+{
+    const int64_t active = m < e ? m : e, rows = (m + active - 1) / active;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    const bool ring = aligned && k % 64 == 0 && k >= 256 && k <= (1 << 22) && xr <= ((int64_t)1 << 30) / k;
+    const ExpertPlan st = stream_plan(active, n, k);
+    if (rows <= (ring ? 2 : 8) && st.fits(m, e, n))
+        return st;
+    auto fills = [&](const ExpertPlan& p, int64_t least) {
+        return (n + p.a - 1) / p.a * active * ((rows + p.b - 1) / p.b) >= least && p.fits(m, e, n);
+    };
+    if (ring) {
+        const int bm = rows <= 16 ? 32 : (rows <= 48 ? 64 : (rows <= 192 ? 128 : 256));
+        for (const ExpertPlan& p : kRings) {
+            if (p.b > bm || (p.a == 256 && p.b == 32 && k < 2048))
+                continue;
+            if (fills(p, p.b == 256 ? 128 : 224))
+                return p;
+        }
+        for (const ExpertPlan& p : kRings)  // a small layer: the narrowest tile for these rows
+            if (p.a == 64 && p.b <= bm && p.fits(m, e, n))
+                return p;
+    }
+    for (const ExpertPlan& p : kTiles)
+        if (p.b <= (rows <= 64 ? 64 : 128) && fills(p, 224))
+            return p;
+    return {ExpertKind::TILE, 64, 64, 4};
+}
+
 template <typename A, int CT, int W>
-hipError_t launch_stream(const ExpertCall& c, hipStream_t stream)
+hipError_t run_stream(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + 16 * CT - 1) / (16 * CT), groups = TN * max_row_tiles(c.m, c.e, 16);
     hipLaunchKernelGGL((experts_stream_kernel<A, CT, W>), dim3((unsigned)groups), dim3(W * kWave), 0, stream, c,
@@ -263,41 +618,52 @@ hipError_t launch_stream(const ExpertCall& c, hipStream_t stream)
     return hipGetLastError();
 }
 
-struct ExpertPlan {
-    bool stream;
-    int ct, w;
-};
-
-ExpertPlan experts_plan(int64_t m, int64_t e, int64_t n, int64_t k)
+template <typename A, int BN, int BM, int WN, int WM>
+hipError_t run_tile(const ExpertCall& c, hipStream_t stream)
 {
-    const int64_t active = m < e ? m : e;  // at most so many experts have rows
-    ExpertPlan p{m <= 16 * active, 4, 8};
-    const int64_t tiles = max_row_tiles(m, e, 16);
-    auto groups = [&](int ct) { return (n + 16 * ct - 1) / (16 * ct) * active; };
-    while (p.ct > 1 && groups(p.ct) < 256)
-        p.ct /= 2;
-    p.w = k >= 2048 ? 8 : 4;
-    if (!grid_fits((n + 16 * p.ct - 1) / (16 * p.ct) * tiles, p.w * kWave))
-        p.stream = false;
-    return p;
+    const int64_t TN = (c.n + BN - 1) / BN, groups = TN * max_row_tiles(c.m, c.e, BM);
+    hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM>), dim3((unsigned)groups), dim3(WN * WM * kWave), 0,
+                       stream, c, (int)TN);
+    return hipGetLastError();
+}
+
+template <typename A, int BN, int BM, int WN, int WM>
+hipError_t run_ring(const ExpertCall& c, hipStream_t stream)
+{
+    const int64_t TN = (c.n + BN - 1) / BN, groups = TN * max_row_tiles(c.m, c.e, BM);
+    hipLaunchKernelGGL((experts_ring_kernel<A, BN, BM, WN, WM, ring_depth(BN, BM)>), dim3((unsigned)groups),
+                       dim3(WN * WM * kWave), 0, stream, c, (int)TN);
+    return hipGetLastError();
 }
 
 template <typename A>
 hipError_t launch_typed(const ExpertCall& c, hipStream_t stream)
 {
-    const ExpertPlan p = experts_plan(c.m, c.e, c.n, c.k);
-    if (p.stream) {
+    const ExpertPlan p = experts_plan(c.m, c.e, c.n, c.k, c.xr, c.x, c.q);
+    if (p.kind == ExpertKind::STREAM) {
         if (p.w == 8)
-            return p.ct == 4   ? launch_stream<A, 4, 8>(c, stream)
-                   : p.ct == 2 ? launch_stream<A, 2, 8>(c, stream)
-                               : launch_stream<A, 1, 8>(c, stream);
-        return p.ct == 4   ? launch_stream<A, 4, 4>(c, stream)
-               : p.ct == 2 ? launch_stream<A, 2, 4>(c, stream)
-                           : launch_stream<A, 1, 4>(c, stream);
+            return p.a == 4   ? run_stream<A, 4, 8>(c, stream)
+                   : p.a == 2 ? run_stream<A, 2, 8>(c, stream)
+                              : run_stream<A, 1, 8>(c, stream);
+        return p.a == 4   ? run_stream<A, 4, 4>(c, stream)
+               : p.a == 2 ? run_stream<A, 2, 4>(c, stream)
+                          : run_stream<A, 1, 4>(c, stream);
     }
-    const int64_t TN = (c.n + 63) / 64, groups = TN * max_row_tiles(c.m, c.e, 64);
-    hipLaunchKernelGGL(experts_any_kernel<A>, dim3((unsigned)groups), dim3(256), 0, stream, c, (int)TN);
-    return hipGetLastError();
+    if (p.kind == ExpertKind::TILE)
+        return p.a == 256   ? run_tile<A, 256, 128, 2, 4>(c, stream)
+               : p.a == 128 ? run_tile<A, 128, 64, 2, 2>(c, stream)
+                            : run_tile<A, 64, 64, 2, 2>(c, stream);
+    if (p.b == 256)
+        return run_ring<A, 256, 256, 2, 4>(c, stream);
+    if (p.b == 128)
+        return p.a == 256 ? run_ring<A, 256, 128, 4, 2>(c, stream) : run_ring<A, 128, 128, 4, 2>(c, stream);
+    if (p.b == 64)
+        return p.a == 256   ? run_ring<A, 256, 64, 4, 2>(c, stream)
+               : p.a == 128 ? run_ring<A, 128, 64, 2, 2>(c, stream)
+                            : run_ring<A, 64, 64, 2, 2>(c, stream);
+    return p.a == 256   ? run_ring<A, 256, 32, 4, 1>(c, stream)
+           : p.a == 128 ? run_ring<A, 128, 32, 4, 1>(c, stream)
+                        : run_ring<A, 64, 32, 2, 1>(c, stream);
 }
 
 }  // namespace
@@ -312,13 +678,15 @@ hipError_t launch_experts(const ExpertCall& c, Act act, void*, size_t, hipStream
     return act == Act::BF16 ? launch_typed<Bf16>(c, stream) : launch_typed<F16>(c, stream);
 }
 
-const char* experts_kernel_name(int64_t m, int64_t e, int64_t n, int64_t k, const void*, const uint8_t*)
+const char* experts_kernel_name(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q)
 {
     thread_local char name[96];
-    const ExpertPlan p = experts_plan(m, e, n, k);
-    if (!p.stream)
-        return "experts_any_kernel";
-    snprintf(name, sizeof name, "experts_stream_kernel<CT=%d,W=%d>", p.ct, p.w);
+    const ExpertPlan p = experts_plan(m, e, n, k, m, x, q);
+    if (p.kind == ExpertKind::STREAM)
+        snprintf(name, sizeof name, "experts_stream_kernel<CT=%d,W=%d>", p.a, p.w);
+    else
+        snprintf(name, sizeof name, "experts_%s_kernel<BN=%d,BM=%d,W=%d>",
+                 p.kind == ExpertKind::TILE ? "tile" : "ring", p.a, p.b, p.w);
     return name;
 }
 

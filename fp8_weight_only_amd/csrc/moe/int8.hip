@@ -631,16 +631,17 @@ struct Int8Ring {
     }
     __device__ __forceinline__ void read(const uint8_t* buf, int j, Frags& f) const
     {
-        // fragment q's row is 32 q further: the same rotation
+        // fragment q's row is 32 q further: the same rotation. One addition to the buffer's
+        // address per read: through longer chains the compiler loses which buffer is read,
+        // and waits for every load in flight
         const int i = lane & 31, c = 16 * ((2 * j + (lane >> 5) + (i >> 2)) & 3);
-        const uint8_t* pa = buf + 64 * (wn * (BN / WN) + i) + c;
-        const uint8_t* px = buf + 64 * (BN + wm * (BM / WM) + i) + c;
+        const int oa = 64 * (wn * (BN / WN) + i) + c, ox = 64 * (BN + wm * (BM / WM) + i) + c;
 #pragma unroll
         for (int q = 0; q < FN; ++q)
-            f.a[q] = *reinterpret_cast<const i32x4*>(pa + 2048 * q);
+            f.a[q] = *reinterpret_cast<const i32x4*>(buf + (oa + 2048 * q));
 #pragma unroll
         for (int q = 0; q < FM; ++q)
-            f.x[q] = *reinterpret_cast<const i32x4*>(px + 2048 * q);
+            f.x[q] = *reinterpret_cast<const i32x4*>(buf + (ox + 2048 * q));
     }
     __device__ __forceinline__ void mma(const Frags& f, i32x16* acc) const
     {

@@ -80,8 +80,8 @@ FP8W_API fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype
 FP8W_API size_t fp8w_linear_experts_workspace_bytes(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                     const uint8_t* q);
 
-/* Name of the kernel fp8w_linear_experts runs (with its workspace), NULL for
- * invalid sizes and calls that run none. The string lives until the thread's
+/* Name of the kernel fp8w_linear_experts runs for an x of up to m rows (with its
+ * workspace), NULL for invalid sizes and calls that run none. The string lives until the thread's
  * next call. */
 FP8W_API const char* fp8w_linear_experts_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                 const uint8_t* q);
