@@ -122,13 +122,13 @@ fp8w_status_t fp8w_route(const void* logits, fp8w_dtype_t dtype, int64_t t, int6
     if (!aligned(logits, elem_bytes(dtype)) || !aligned(weights, 4) || !aligned(experts, 4) || !aligned(offsets, 4) ||
         !aligned(slots, 4) || !aligned(tokens, 4))
         return FP8W_ERR_MISALIGNED;
-    const size_t need = fp8w::route_workspace_bytes(t, e, top_k);
-    if (need > 0) {
-        if (!workspace || workspace_bytes < need)
-            return FP8W_ERR_WORKSPACE;
-        if (!aligned(workspace, 4))
-            return FP8W_ERR_MISALIGNED;
-    }
+    size_t need = fp8w::route_workspace_bytes(t, e, top_k);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return FP8W_ERR_WORKSPACE;
+    if (!aligned(workspace, 4))
+        return FP8W_ERR_MISALIGNED;
+    if (need == 0 && workspace_bytes > 0)
+        need = 1;  // one that is passed without need is not an output's place either
     const size_t lists = t > 0 ? (size_t)t * (size_t)top_k * 4 : 0;
     const Span all[] = {{logits, (size_t)t * (size_t)e * elem_bytes(dtype)}, {weights, lists}, {experts, lists},
                         {offsets, ((size_t)e + 1) * 4}, {slots, lists}, {tokens, lists}, {workspace, need}};

@@ -13,7 +13,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename A>
+// TOP > 0: top, known when compiled; 0: any.
+template <typename A, int TOP>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __restrict__ y,
                                                            const float* __restrict__ weights,
                                                            uint16_t* __restrict__ out, int64_t items, int top,
@@ -30,15 +31,25 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         acc[i] = 0.0f;
-    for (int j = 0; j < top; ++j) {
-        const u32x4 v = load16_part(reinterpret_cast<const uint8_t*>(src + j * n), left);
-        const float wj = w[j];
+    auto add = [&](u32x4 v, float wj) {
         const uint32_t d[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             acc[2 * i] = __builtin_fmaf(wj, A::lo_f32(d[i]), acc[2 * i]);
             acc[2 * i + 1] = __builtin_fmaf(wj, A::hi_f32(d[i]), acc[2 * i + 1]);
         }
+    };
+    if constexpr (TOP > 0) {
+        u32x4 v[TOP];
+#pragma unroll
+        for (int j = 0; j < TOP; ++j)
+            v[j] = left >= 16 ? load16_once(src + j * n) : load16_part(reinterpret_cast<const uint8_t*>(src + j * n), left);
+#pragma unroll
+        for (int j = 0; j < TOP; ++j)
+            add(v[j], w[j]);
+    } else {
+        for (int j = 0; j < top; ++j)
+            add(load16_part(reinterpret_cast<const uint8_t*>(src + j * n), left), w[j]);
     }
     uint16_t o[8];
 #pragma unroll
@@ -68,13 +79,27 @@ hipError_t launch_combine(const void* y, Act act, const float* weights, int64_t 
     const int64_t chunks = (n + 7) / 8, items = t * chunks, groups = (items + kThreads - 1) / kThreads;
     if (!grid_fits(groups, kThreads))
         return hipErrorInvalidValue;
+    const uint16_t* src = static_cast<const uint16_t*>(y);
+    uint16_t* dst = static_cast<uint16_t*>(out);
     const dim3 grid((unsigned)groups), block(kThreads);
-    if (act == Act::BF16)
-        hipLaunchKernelGGL(combine_kernel<Bf16>, grid, block, 0, stream, static_cast<const uint16_t*>(y), weights,
-                           static_cast<uint16_t*>(out), items, (int)top, n, chunks);
-    else
-        hipLaunchKernelGGL(combine_kernel<F16>, grid, block, 0, stream, static_cast<const uint16_t*>(y), weights,
-                           static_cast<uint16_t*>(out), items, (int)top, n, chunks);
+#define FP8W_COMBINE(A, TOP)                                                                                           \
+    hipLaunchKernelGGL((combine_kernel<A, TOP>), grid, block, 0, stream, src, weights, dst, items, (int)top, n, chunks)
+#define FP8W_COMBINE_TOP(A)                                                                                            \
+    switch (top) {                                                                                                     \
+    case 1: FP8W_COMBINE(A, 1); break;                                                                                 \
+    case 2: FP8W_COMBINE(A, 2); break;                                                                                 \
+    case 4: FP8W_COMBINE(A, 4); break;                                                                                 \
+    case 6: FP8W_COMBINE(A, 6); break;                                                                                 \
+    case 8: FP8W_COMBINE(A, 8); break;                                                                                 \
+    default: FP8W_COMBINE(A, 0);                                                                                       \
+    }
+    if (act == Act::BF16) {
+        FP8W_COMBINE_TOP(Bf16)
+    } else {
+        FP8W_COMBINE_TOP(F16)
+    }
+#undef FP8W_COMBINE_TOP
+#undef FP8W_COMBINE
     return hipGetLastError();
 }
 

@@ -18,6 +18,12 @@ __device__ __forceinline__ u32x4 load16_any(const void* p)
     return *static_cast<const u32x4_any*>(p);
 }
 
+// The same for data that is read once.
+__device__ __forceinline__ u32x4 load16_once(const void* p)
+{
+    return __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
+}
+
 __device__ __forceinline__ void store16_any(void* p, u32x4 v)
 {
     *static_cast<u32x4_any*>(p) = v;
@@ -81,6 +87,14 @@ __device__ __forceinline__ const uint8_t* uniform(const void* p)
     const uint64_t v = reinterpret_cast<uint64_t>(p);
     const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(uint32_t)(v >> 32));
     return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+}
+
+// Between one lane's LDS write and another lane's read in the same wave: LDS
+// works in order, so only the compiler has to keep it.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Tile (tn, tm) of linear workgroup id L < TN * TM. Workgroups are dealt to the

@@ -130,6 +130,10 @@ def fp8w_moe_last_hip_error() -> int:
 
 
 # ------------------------------------------------------------------ tensor helpers
+# A call costs the host as long as a small one costs the GPU, so the helpers look at each tensor once.
+# The handle of a device's current stream, without the stream object that torch.cuda.current_stream makes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _STATUS = ("success", "invalid value (size, dtype, NULL pointer or overlapping buffers)", "misaligned pointer",
            "non-finite weight (NaN or infinity)", "workspace missing or too small", "HIP runtime error")
@@ -162,11 +166,11 @@ def _want(t, name: str, shape, dtype, device) -> int:
     """The device address of a tensor that must look like this (0 for None and empty ones)."""
     if t is None:
         return 0
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be on the GPU of the first argument")
-    if not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{name} must be {list(shape)} of {dtype}, not {list(t.shape)} of {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on the GPU of the first argument")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr() if t.numel() else 0
 
@@ -191,7 +195,7 @@ def _workspace(ws, need: int, device):
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 class Route(NamedTuple):
@@ -218,18 +222,26 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Route
     if not 1 <= top_k <= min(e, 64) or e > 1024:
         raise ValueError("expected 1 <= top_k <= min(e, 64) and e <= 1024")
     lp = _want(logits, "logits", (t, e), logits.dtype, dev)
+    need = fp8w_route_workspace_bytes(t, e, top_k)
     if out is None:
-        # one allocation for the integer results
-        ints = torch.empty((3 * t * top_k + e + 1,), dtype=torch.int32, device=dev)
-        a, b, c = t * top_k, 2 * t * top_k, 3 * t * top_k
-        out = Route(torch.empty((t, top_k), dtype=torch.float32, device=dev), ints[:a].view(t, top_k), ints[c:],
-                    ints[a:b], ints[b:c])
-    ptr = [_want(out.weights, "weights", (t, top_k), torch.float32, dev),
-           _want(out.experts, "experts", (t, top_k), torch.int32, dev),
-           _want(out.offsets, "offsets", (e + 1,), torch.int32, dev),
-           _want(out.slots, "slots", (t * top_k,), torch.int32, dev),
-           _want(out.tokens, "tokens", (t * top_k,), torch.int32, dev)]
-    workspace, wp, wb = _workspace(workspace, fp8w_route_workspace_bytes(t, e, top_k), dev)
+        # one allocation: weights, experts, slots, tokens, offsets, and the workspace if none is passed
+        a = t * top_k
+        own = need // 4 if workspace is None else 0
+        buf = logits.new_empty((4 * a + e + 1 + own,), dtype=torch.int32)
+        parts = buf.split([a, a, a, a, e + 1, own])
+        out = Route(parts[0].view(torch.float32).view(t, top_k), parts[1].view(t, top_k), parts[4], parts[2], parts[3])
+        base = buf.data_ptr()
+        ptr = [base, base + 4 * a, base + 16 * a, base + 8 * a, base + 12 * a] if t else [0, 0, base, 0, 0]
+        wp, wb = (base + 4 * (4 * a + e + 1), need) if workspace is None else (0, 0)
+    else:
+        ptr = [_want(out.weights, "weights", (t, top_k), torch.float32, dev),
+               _want(out.experts, "experts", (t, top_k), torch.int32, dev),
+               _want(out.offsets, "offsets", (e + 1,), torch.int32, dev),
+               _want(out.slots, "slots", (t * top_k,), torch.int32, dev),
+               _want(out.tokens, "tokens", (t * top_k,), torch.int32, dev)]
+        wp = None
+    if workspace is not None or wp is None:
+        workspace, wp, wb = _workspace(workspace, need, dev)
     st = fp8w_route(lp, _DT[logits.dtype], t, e, top_k, int(renormalize), *ptr, wp, wb, _stream(dev))
     _check(st, "fp8w_route")
     return out
@@ -276,7 +288,7 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     ip = _want(x_rows, "x_rows", (m,), torch.int32, dev)
     jp = _want(y_rows, "y_rows", (m,), torch.int32, dev)
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=dev)
+        out = x.new_empty((m, n))
     yp = _want(out, "out", (m, n), x.dtype, dev)
     need = fp8w_linear_experts_workspace_bytes(m, e, n, k, xp, qp)
     workspace, wp, wb = _workspace(workspace, need, dev)
@@ -297,7 +309,7 @@ def combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor = None) ->
     yp = _want(y, "y", (t * top, n), y.dtype, dev)
     wp = _want(weights, "weights", (t, top), torch.float32, dev)
     if out is None:
-        out = torch.empty((t, n), dtype=y.dtype, device=dev)
+        out = y.new_empty((t, n))
     st = fp8w_combine(yp, act, wp, t, top, n, _want(out, "out", (t, n), y.dtype, dev), _stream(dev))
     _check(st, "fp8w_combine")
     return out
@@ -367,7 +379,7 @@ def linear_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
     sp = _want(scale, "scale", (n,), torch.float32, dev)
     bp = _want(bias, "bias", (n,), x.dtype, dev)
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=dev)
+        out = x.new_empty((m, n))
     yp = _want(out, "out", (m, n), x.dtype, dev)
     workspace, wp, wb = _workspace(workspace, fp8w_linear_int8_workspace_bytes(m, n, k, xp, qp), dev)
     st = fp8w_linear_int8(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, _stream(dev))
