@@ -3,7 +3,9 @@
 Every source under csrc/ is compiled to an object in parallel, then linked into
 ``fp8_weight_only_amd/libfp8w.so`` (the FP8 linear layer, include/fp8w.h); those
 under csrc/moe/ go into ``fp8_weight_only_amd/libfp8w_moe.so`` (routing, products
-grouped by expert, the int8 layer, include/fp8w_moe.h). Flags: -O3, IEEE fp32 division (no
+grouped by expert, the int8 layer, include/fp8w_moe.h), and csrc/moe/helpers.cpp
+(host code only: checks and allocations of that library's tensor helpers) into
+the extension module ``fp8_weight_only_amd/_moe_helpers.so``. Flags: -O3, IEEE fp32 division (no
 fast-math), hidden visibility except the C ABI, packed-fp32 instructions
 disabled (the compiler's own choice of v_pk_*_f32 is switched off), and kernel
 arguments preloaded into SGPRs at wave launch (up to 16 SGPRs' worth). With
@@ -15,16 +17,19 @@ header that loads the arguments itself, for firmware that does not preload.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8w.so")
 MOE_LIB = os.path.join(HERE, "libfp8w_moe.so")
+MOE_HELPERS = os.path.join(HERE, "_moe_helpers.so")
 OBJDIR = os.path.join(ROOT, "_build", "fp8w")
 ARCH = os.environ.get("FP8W_ARCH", "gfx950")
 
@@ -52,16 +57,31 @@ def moe_sources():
     return sorted(glob.glob(os.path.join(CSRC, "moe", "*.hip")))
 
 
+def _torch_dir() -> str:
+    return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _compile_command(src: str, obj: str):
+    if src.endswith(".hip"):
+        return [_hipcc(), *CFLAGS, "-c", src, "-o", obj]
+    torch_include = os.path.join(_torch_dir(), "include")
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(_hipcc())))
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra",
+            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-I", sysconfig.get_paths()["include"], "-isystem",
+            torch_include, "-isystem", os.path.join(torch_include, "torch", "csrc", "api", "include"), "-isystem",
+            os.path.join(rocm, "include"), "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJDIR, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
-    cmd = [_hipcc(), *CFLAGS, "-c", src, "-o", obj]
+    cmd = _compile_command(src, obj)
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     # the host pass does not know the packed-fp32 feature and says so; keep real diagnostics
     out = "\n".join(l for l in r.stdout.splitlines() if "packed-fp32-ops" not in l and l.strip())
     if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {src}:\n{out}")
+        raise RuntimeError(f"{cmd[0]} failed on {src}:\n{out}")
     if out and verbose:
         print(out, flush=True)
     return obj
@@ -76,14 +96,27 @@ def _link(objs, lib: str, verbose: bool) -> None:
     os.replace(tmp, lib)
 
 
+def _link_helpers(obj: str, verbose: bool) -> None:
+    """The extension module; finds libfp8w_moe.so beside itself, torch's libraries in the process."""
+    tmp = MOE_HELPERS + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, "-L", os.path.join(_torch_dir(), "lib"), "-lc10",
+           "-lc10_hip", "-ltorch_cpu", "-ltorch_python", "-L", HERE, "-lfp8w_moe", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MOE_HELPERS)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     libs = [(LIB, sources()), (MOE_LIB, moe_sources())]
-    srcs = [s for _, part in libs for s in part]
+    helpers = os.path.join(CSRC, "moe", "helpers.cpp")
+    srcs = [helpers] + [s for _, part in libs for s in part]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
     for lib, part in libs:
         _link([objs[s] for s in part], lib, verbose)
+    _link_helpers(objs[helpers], verbose)
     return LIB
 
 

@@ -4,7 +4,10 @@ A thin ctypes binding over ``libfp8w_moe.so`` (declared in
 ``include/fp8w_moe.h``), in the manner of the package's FP8 linear layer: the
 raw entry points keep the C names and take integers; the tensor helpers check
 their arguments, allocate outputs and workspaces with torch and run on torch's
-current stream. There is no CPU or PyTorch fallback.
+current stream. The helpers of the timed path go through a small compiled module
+(``csrc/moe/helpers.cpp``), which does the same for calls that are right; the
+Python below it says what is wrong with the others and takes a caller's
+workspace. There is no CPU or PyTorch fallback.
 
     r = route(logits, top_k)                       # who goes where
     h = linear_experts(x, q, scale, r.offsets, x_rows=r.tokens)     # up: gathers tokens, rows by expert
@@ -47,6 +50,7 @@ __all__ = [*MOE_EXPORTS, "MOE_EXPORTS", "Fp8wMoeError", "moe_lib_path", "load_mo
            "quantize_activations_int8", "gemm_int8", "linear_int8", "int8_workspace_bytes"]
 
 _LIB = None
+_FAST = None
 
 
 def moe_lib_path() -> str:
@@ -68,6 +72,20 @@ def load_moe():
             f.argtypes = args
         _LIB = lib
     return _LIB
+
+
+def _fast():
+    """The compiled helpers (raises if they have not been built)."""
+    global _FAST
+    if _FAST is None:
+        load_moe()
+        try:
+            from . import _moe_helpers
+        except ImportError as e:
+            raise RuntimeError("_moe_helpers.so is missing or does not load: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _FAST = _moe_helpers
+    return _FAST
 
 
 # ------------------------------------------------------------------ raw C entry points
@@ -130,7 +148,6 @@ def fp8w_moe_last_hip_error() -> int:
 
 
 # ------------------------------------------------------------------ tensor helpers
-# A call costs the host as long as a small one costs the GPU, so the helpers look at each tensor once.
 # The handle of a device's current stream, without the stream object that torch.cuda.current_stream makes.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -215,6 +232,10 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Route
     ``renormalize``. Equal logits go to the lower index; an expert with logit
     -inf is never taken (its place holds -1 and weight 0), so a row of -inf is a
     padding token. ``out`` takes the results of an earlier call's shape."""
+    if out is None and workspace is None:
+        r = (_FAST or _fast()).route(logits, top_k, renormalize)
+        if r is not None:
+            return Route._make(r)
     dev = _gpu(logits, "logits", 2)
     t, e = logits.shape
     if logits.dtype not in _DT:
@@ -222,26 +243,17 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Route
     if not 1 <= top_k <= min(e, 64) or e > 1024:
         raise ValueError("expected 1 <= top_k <= min(e, 64) and e <= 1024")
     lp = _want(logits, "logits", (t, e), logits.dtype, dev)
-    need = fp8w_route_workspace_bytes(t, e, top_k)
     if out is None:
-        # one allocation: weights, experts, slots, tokens, offsets, and the workspace if none is passed
-        a = t * top_k
-        own = need // 4 if workspace is None else 0
-        buf = logits.new_empty((4 * a + e + 1 + own,), dtype=torch.int32)
-        parts = buf.split([a, a, a, a, e + 1, own])
-        out = Route(parts[0].view(torch.float32).view(t, top_k), parts[1].view(t, top_k), parts[4], parts[2], parts[3])
-        base = buf.data_ptr()
-        ptr = [base, base + 4 * a, base + 16 * a, base + 8 * a, base + 12 * a] if t else [0, 0, base, 0, 0]
-        wp, wb = (base + 4 * (4 * a + e + 1), need) if workspace is None else (0, 0)
-    else:
-        ptr = [_want(out.weights, "weights", (t, top_k), torch.float32, dev),
-               _want(out.experts, "experts", (t, top_k), torch.int32, dev),
-               _want(out.offsets, "offsets", (e + 1,), torch.int32, dev),
-               _want(out.slots, "slots", (t * top_k,), torch.int32, dev),
-               _want(out.tokens, "tokens", (t * top_k,), torch.int32, dev)]
-        wp = None
-    if workspace is not None or wp is None:
-        workspace, wp, wb = _workspace(workspace, need, dev)
+        out = Route(logits.new_empty((t, top_k), dtype=torch.float32),
+                    logits.new_empty((t, top_k), dtype=torch.int32), logits.new_empty((e + 1,), dtype=torch.int32),
+                    logits.new_empty((t * top_k,), dtype=torch.int32),
+                    logits.new_empty((t * top_k,), dtype=torch.int32))
+    ptr = [_want(out.weights, "weights", (t, top_k), torch.float32, dev),
+           _want(out.experts, "experts", (t, top_k), torch.int32, dev),
+           _want(out.offsets, "offsets", (e + 1,), torch.int32, dev),
+           _want(out.slots, "slots", (t * top_k,), torch.int32, dev),
+           _want(out.tokens, "tokens", (t * top_k,), torch.int32, dev)]
+    workspace, wp, wb = _workspace(workspace, fp8w_route_workspace_bytes(t, e, top_k), dev)
     st = fp8w_route(lp, _DT[logits.dtype], t, e, top_k, int(renormalize), *ptr, wp, wb, _stream(dev))
     _check(st, "fp8w_route")
     return out
@@ -273,6 +285,10 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     bias: [e, n] of x.dtype; offsets: [e + 1] int32; x_rows / y_rows: [m] int32
     (without them position p reads row p / writes row p). Rows of positions from
     offsets[e] on are zeros. With ``x_rows`` m is its length, else x's."""
+    if workspace is None:
+        r = (_FAST or _fast()).linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out)
+        if r is not None:
+            return r
     dev = _gpu(x, "x", 2)
     if q.dim() != 3:
         raise ValueError("q must have 3 dimensions")
@@ -300,6 +316,9 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
 def combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor = None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[t * top_k + j], fp32 sums, rounded once:
     y [t * top_k, n] bf16 / fp16 (rows by slot), weights [t, top_k] fp32."""
+    r = (_FAST or _fast()).combine(y, weights, out)
+    if r is not None:
+        return r
     dev = _gpu(y, "y", 2)
     if weights.dim() != 2:
         raise ValueError("weights must have 2 dimensions")
@@ -370,6 +389,10 @@ def linear_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
     """The int8 layer on bf16 / fp16 activations x [m, k]: per-token quantization
     of x, integer products with q int8 [n, k], y = sums * sx * scale + bias
     rounded once to x.dtype."""
+    if workspace is None:
+        r = (_FAST or _fast()).linear_int8(x, q, scale, bias, out)
+        if r is not None:
+            return r
     dev = _gpu(x, "x", 2)
     m, k = x.shape
     n = q.shape[0]
