@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 256;
 
 // TOP > 0: top, known when compiled; 0: any.
-template <typename A, int TOP>
+template <typename A, int TOP, bool SHIFT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __restrict__ y,
                                                            const float* __restrict__ weights,
                                                            uint16_t* __restrict__ out, int64_t items, int top,
@@ -41,9 +41,25 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
     };
     if constexpr (TOP > 0) {
         u32x4 v[TOP];
+        if (left >= 16) {
+            if constexpr (SHIFT) {
+                typename Row<true>::Raw raw[TOP];
 #pragma unroll
-        for (int j = 0; j < TOP; ++j)
-            v[j] = left >= 16 ? load16_once(src + j * n) : load16_part(reinterpret_cast<const uint8_t*>(src + j * n), left);
+                for (int j = 0; j < TOP; ++j)
+                    raw[j] = Row<true>(src + j * n).load(0);
+#pragma unroll
+                for (int j = 0; j < TOP; ++j)
+                    v[j] = Row<true>(src + j * n).bytes(raw[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < TOP; ++j)
+                    v[j] = load16_once(src + j * n);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < TOP; ++j)
+                v[j] = load16_part(reinterpret_cast<const uint8_t*>(src + j * n), left);
+        }
 #pragma unroll
         for (int j = 0; j < TOP; ++j)
             add(v[j], w[j]);
@@ -54,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __res
     uint16_t o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        o[i] = A::from_f32(acc[i]);
+        o[i] = rounded<A>(acc[i]);
     uint16_t* dst = out + t * n + c;
     if (left >= 16) {
         u32x4 pk;
@@ -81,9 +97,15 @@ hipError_t launch_combine(const void* y, Act act, const float* weights, int64_t 
         return hipErrorInvalidValue;
     const uint16_t* src = static_cast<const uint16_t*>(y);
     uint16_t* dst = static_cast<uint16_t*>(out);
+    const bool shift = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(2 * n)) & 3) != 0;
     const dim3 grid((unsigned)groups), block(kThreads);
 #define FP8W_COMBINE(A, TOP)                                                                                           \
-    hipLaunchKernelGGL((combine_kernel<A, TOP>), grid, block, 0, stream, src, weights, dst, items, (int)top, n, chunks)
+    if (shift)                                                                                                         \
+        hipLaunchKernelGGL((combine_kernel<A, TOP, true>), grid, block, 0, stream, src, weights, dst, items, (int)top, \
+                           n, chunks);                                                                                 \
+    else                                                                                                               \
+        hipLaunchKernelGGL((combine_kernel<A, TOP, false>), grid, block, 0, stream, src, weights, dst, items,          \
+                           (int)top, n, chunks)
 #define FP8W_COMBINE_TOP(A)                                                                                            \
     switch (top) {                                                                                                     \
     case 1: FP8W_COMBINE(A, 1); break;                                                                                 \

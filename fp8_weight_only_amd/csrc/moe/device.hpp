@@ -12,6 +12,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // 16 bytes at any address (the hardware takes unaligned global accesses).
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x4_dword __attribute__((ext_vector_type(4), aligned(4)));  // at any dword
+typedef uint32_t u32x2_dword __attribute__((ext_vector_type(2), aligned(4)));
 
 __device__ __forceinline__ u32x4 load16_any(const void* p)
 {
@@ -56,6 +58,75 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+// A row that is read 16 bytes at a time. SHIFT: it may start at any byte; the
+// loads then are of whole aligned dwords, four and the one behind them, shifted
+// together. The hardware takes any address, but below dword alignment at 0.4 of
+// the rate ([14336, 4100] codes streamed in 26 us, [14336, 4098] in 58). No dword
+// is read that holds no byte of the 16.
+//
+// load() requests them, bytes() puts them together once they are needed.
+template <bool SHIFT>
+struct Row {
+    struct Raw {
+        u32x4 v;
+        uint32_t e[SHIFT ? 1 : 0];
+    };
+    const uint8_t* p;
+    uint32_t shift, behind;
+
+    Row() = default;
+    __device__ __forceinline__ explicit Row(const void* start) : p(static_cast<const uint8_t*>(start))
+    {
+        if constexpr (SHIFT) {
+            shift = (uint32_t)reinterpret_cast<uintptr_t>(start) & 3u;
+            p -= shift;
+            behind = shift ? 16 : 0;
+        }
+    }
+    // the 16 bytes at off, a multiple of 4
+    __device__ __forceinline__ Raw load(int64_t off) const
+    {
+        Raw r;
+        if constexpr (SHIFT) {
+            r.v = *reinterpret_cast<const u32x4_dword*>(p + off);
+            r.e[0] = *reinterpret_cast<const uint32_t*>(p + off + behind);
+        } else {
+            r.v = load16_any(p + off);
+        }
+        return r;
+    }
+    __device__ __forceinline__ u32x4 bytes(const Raw& r) const
+    {
+        const u32x4 v = r.v;
+        if constexpr (SHIFT)
+            return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, shift), __builtin_amdgcn_alignbyte(v.z, v.y, shift),
+                         __builtin_amdgcn_alignbyte(v.w, v.z, shift), __builtin_amdgcn_alignbyte(r.e[0], v.w, shift)};
+        return v;
+    }
+    // the first `avail` of them, zeros after
+    __device__ __forceinline__ u32x4 part(int64_t off, int64_t avail) const
+    {
+        return load16_part(p + (SHIFT ? shift : 0) + off, avail);
+    }
+    // the same for bytes() to put together: only for rows with a stage of their own
+    __device__ __forceinline__ Raw part_raw(int64_t off, int64_t avail) const
+    {
+        const u32x4 v = part(off, avail);
+        Raw r;
+        if constexpr (SHIFT) {
+            // moved up by the shift that bytes() takes back
+            const uint32_t back = 4 - shift;
+            r.v = shift ? u32x4{__builtin_amdgcn_alignbyte(v.x, 0, back), __builtin_amdgcn_alignbyte(v.y, v.x, back),
+                                __builtin_amdgcn_alignbyte(v.z, v.y, back), __builtin_amdgcn_alignbyte(v.w, v.z, back)}
+                        : v;
+            r.e[0] = shift ? __builtin_amdgcn_alignbyte(0, v.w, back) : 0;
+        } else {
+            r.v = v;
+        }
+        return r;
+    }
+};
+
 template <typename A>
 struct is_bf16 {
     static constexpr bool value = false;
@@ -64,6 +135,17 @@ template <>
 struct is_bf16<Bf16> {
     static constexpr bool value = true;
 };
+
+// An fp32 result to the activation type. The empty statement keeps the compiler
+// from fusing the last operation with the rounding to fp16 (v_fma_mix rounds
+// once where the two instructions round twice): it did so for some elements of
+// a kernel and not for others, and a call's bits then depended on the plan.
+template <typename A>
+__device__ __forceinline__ uint16_t rounded(float v)
+{
+    asm("" : "+v"(v));
+    return A::from_f32(v);
+}
 
 template <typename A>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
@@ -76,7 +158,10 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
                                                       0, 0, 0);
 }
 
-// A value that is the same in all lanes, in a scalar register.
+// A value that is the same in all lanes, in a scalar register. Whatever decides
+// whether a matrix instruction runs has to be one: those instructions take no
+// notice of masked lanes, and a branch on a per-lane register may be compiled to
+// a mask alone.
 __device__ __forceinline__ int uniform(int v)
 {
     return __builtin_amdgcn_readfirstlane(v);
@@ -114,20 +199,24 @@ __device__ __forceinline__ void xcd_tile(int L, int TN, int TM, int& tn, int& tm
     tn = uniform(w / gs);
 }
 
-// Four consecutive channels of one token: one 8-byte store where it is aligned
-// and all four exist.
+// Four consecutive channels of one token (`left` of them exist): one 8-byte store
+// at dword alignment, else a dword between two halves.
 __device__ __forceinline__ void store4(uint16_t* dst, const uint16_t* o, int64_t left)
 {
-    if (left >= 4 && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+    if (left < 4) {
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (r < left)
+                dst[r] = o[r];
+    } else if ((reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
         u32x2 pk;
         pk.x = (uint32_t)o[0] | ((uint32_t)o[1] << 16);
         pk.y = (uint32_t)o[2] | ((uint32_t)o[3] << 16);
-        *reinterpret_cast<u32x2*>(dst) = pk;
+        *reinterpret_cast<u32x2_dword*>(dst) = pk;
     } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (r < left)
-                dst[r] = o[r];
+        dst[0] = o[0];
+        *reinterpret_cast<uint32_t*>(dst + 1) = (uint32_t)o[1] | ((uint32_t)o[2] << 16);
+        dst[3] = o[3];
     }
 }
 

@@ -45,7 +45,8 @@ __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos,
             continue;
         }
         const int64_t ch = (int64_t)expert * c.n + c0 + r;
-        o[r] = epilogue<A>(ok ? acc[r] : __builtin_nanf(""), c.scale[ch], bias, ch);
+        o[r] = rounded<A>(
+            __builtin_fmaf(c.scale[ch], ok ? acc[r] : __builtin_nanf(""), A::to_f32(bias_bits(bias, ch))));
     }
     store4(out, o, count);
 }
@@ -64,7 +65,7 @@ __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos,
 //
 // Any k and any alignment: whole blocks take unaligned 16-byte loads, the last
 // k % 128 a masked step.
-template <typename A, int CT, int W>
+template <typename A, int CT, int W, bool SHIFT>
 __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, int TN)
 {
     __shared__ __attribute__((aligned(16))) f32x4 part[W][CT][kWave];
@@ -73,49 +74,52 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
     const RowTile tile = finder.find(blockIdx.x / TN);
     if (tile.expert < 0)
         return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)tn * (16 * CT);
     f32x4 acc[CT];
 #pragma unroll
     for (int t = 0; t < CT; ++t)
         acc[t] = f32x4{0.0f};
     if (tile.expert < (int)c.e && c.xr > 0) {
-        const uint8_t* wp[CT];
+        Row<SHIFT> wp[CT], xp;
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             const int64_t ch = n0 + 16 * t + r < c.n ? n0 + 16 * t + r : c.n - 1;
-            wp[t] = c.q + ((int64_t)tile.expert * c.n + ch) * c.k + 16 * g;
+            wp[t] = Row<SHIFT>(c.q + ((int64_t)tile.expert * c.n + ch) * c.k + 16 * g);
         }
         int64_t src = tile.row + (r < tile.rows ? r : 0);  // rows past the tile's: any row, not stored
         if (c.x_rows)
             src = c.x_rows[src];
         if (src < 0 || src >= c.xr)
             src = 0;  // stored as NaN
-        const uint8_t* xp = static_cast<const uint8_t*>(c.x) + 2 * (src * c.k + 16 * g);
+        xp = Row<SHIFT>(static_cast<const uint8_t*>(c.x) + 2 * (src * c.k + 16 * g));
         struct Block {
-            u32x4 w[CT][2], x[2][2];
+            typename Row<SHIFT>::Raw w[CT][2], x[2][2];
         };
         auto load = [&](Block& b, int64_t kb) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int t = 0; t < CT; ++t)
-                    b.w[t][h] = load16_any(wp[t] + kb + 64 * h);
-                b.x[h][0] = load16_any(xp + 2 * kb + 128 * h);
-                b.x[h][1] = load16_any(xp + 2 * kb + 128 * h + 16);
+                    b.w[t][h] = wp[t].load(kb + 64 * h);
+                b.x[h][0] = xp.load(2 * kb + 128 * h);
+                b.x[h][1] = xp.load(2 * kb + 128 * h + 16);
             }
         };
         auto compute = [&](const Block& b) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 x0 = xp.bytes(b.x[h][0]), x1 = xp.bytes(b.x[h][1]);
 #pragma unroll
                 for (int t = 0; t < CT; ++t) {
-                    const u32x4 v = b.w[t][h];
+                    const u32x4 v = wp[t].bytes(b.w[t][h]);
                     const u32x2 d0 = A::decode4(v.x), d1 = A::decode4(v.y), d2 = A::decode4(v.z), d3 = A::decode4(v.w);
-                    acc[t] = A::mfma(u32x4{d0.x, d0.y, d1.x, d1.y}, b.x[h][0], acc[t]);
-                    acc[t] = A::mfma(u32x4{d2.x, d2.y, d3.x, d3.y}, b.x[h][1], acc[t]);
+                    acc[t] = A::mfma(u32x4{d0.x, d0.y, d1.x, d1.y}, x0, acc[t]);
+                    acc[t] = A::mfma(u32x4{d2.x, d2.y, d3.x, d3.y}, x1, acc[t]);
                 }
+            }
         };
+        // this wave's blocks: wave, wave + W, .. below k / 128
         const int64_t whole = c.k / 128;
         int64_t b = wave;
         if (b < whole) {
@@ -134,11 +138,11 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const int64_t left = c.k - kb - 64 * h - 16 * g;
-                const u32x4 x0 = load16_part(xp + 2 * kb + 128 * h, 2 * left);
-                const u32x4 x1 = load16_part(xp + 2 * kb + 128 * h + 16, 2 * left - 16);
+                const u32x4 x0 = xp.part(2 * kb + 128 * h, 2 * left);
+                const u32x4 x1 = xp.part(2 * kb + 128 * h + 16, 2 * left - 16);
 #pragma unroll
                 for (int t = 0; t < CT; ++t) {
-                    const u32x4 v = load16_part(wp[t] + kb + 64 * h, left);
+                    const u32x4 v = wp[t].part(kb + 64 * h, left);
                     const u32x2 d0 = A::decode4(v.x), d1 = A::decode4(v.y), d2 = A::decode4(v.z), d3 = A::decode4(v.w);
                     acc[t] = A::mfma(u32x4{d0.x, d0.y, d1.x, d1.y}, x0, acc[t]);
                     acc[t] = A::mfma(u32x4{d2.x, d2.y, d3.x, d3.y}, x1, acc[t]);
@@ -300,7 +304,7 @@ __device__ __forceinline__ void store_tile(const ExpertCall& c, const ExpertTile
                 uint16_t o[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    o[r] = A::from_f32(bad ? __builtin_nanf("")
+                    o[r] = rounded<A>(bad ? __builtin_nanf("")
                                            : __builtin_fmaf(s4[r], acc[fn * P::FM + fm][4 * j + r], bf[r]));
                 if (c0 < c.n)
                     store4(out + c0, o, c.n - c0);
@@ -328,7 +332,7 @@ __device__ __forceinline__ bool find_tile(const ExpertCall& c, int TN, int& tn, 
 // Any k, any alignment, any number of rows in x: a stage passes through
 // registers into LDS. Stage s + 2 is requested when stage s begins, stage s + 1
 // is written to the other LDS buffer when it ends.
-template <typename A, int BN, int BM, int WN, int WM>
+template <typename A, int BN, int BM, int WN, int WM, bool SHIFT>
 __global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall c, int TN)
 {
     using P = ExpertTile<A, BN, BM, WN, WM>;
@@ -354,49 +358,49 @@ __global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall 
         acc[f] = f32x16{0.0f};
     const int64_t S = tile.expert < (int)c.e && c.xr > 0 ? (c.k + 63) / 64 : 0;
     if (S > 0) {
-        const uint8_t *wp[LW], *xp[LX];
+        Row<SHIFT> wp[LW], xp[LX];
         int wo[LW], xo[LX];
         const int wc = tid & 3, xc = tid & 7;
 #pragma unroll
         for (int u = 0; u < LW; ++u) {
             const int r = (tid >> 2) + P::NT / 4 * u;
-            wp[u] = c.q + ((int64_t)tile.expert * c.n + (n0 + r < c.n ? n0 + r : c.n - 1)) * c.k + 16 * wc;
+            wp[u] = Row<SHIFT>(c.q + ((int64_t)tile.expert * c.n + (n0 + r < c.n ? n0 + r : c.n - 1)) * c.k + 16 * wc);
             wo[u] = 64 * r + 16 * ((wc + (r >> 2)) & 3);
         }
 #pragma unroll
         for (int u = 0; u < LX; ++u) {
             const int r = (tid >> 3) + P::NT / 8 * u;
-            xp[u] = static_cast<const uint8_t*>(c.x) + 2 * (source_row(c, tile, r) * c.k + 8 * xc);
+            xp[u] = Row<SHIFT>(static_cast<const uint8_t*>(c.x) + 2 * (source_row(c, tile, r) * c.k + 8 * xc));
             xo[u] = P::ABYTES + 128 * r + 16 * ((xc + (r >> 1)) & 7);
         }
         struct Regs {
-            u32x4 w[LW], x[LX];
+            typename Row<SHIFT>::Raw w[LW], x[LX];
         };
         auto load = [&](Regs& g, int64_t s) {
             const int64_t kb = 64 * s;
             if (kb + 64 <= c.k) {
 #pragma unroll
                 for (int u = 0; u < LW; ++u)
-                    g.w[u] = load16_any(wp[u] + kb);
+                    g.w[u] = wp[u].load(kb);
 #pragma unroll
                 for (int u = 0; u < LX; ++u)
-                    g.x[u] = load16_any(xp[u] + 2 * kb);
+                    g.x[u] = xp[u].load(2 * kb);
             } else {
 #pragma unroll
                 for (int u = 0; u < LW; ++u)
-                    g.w[u] = load16_part(wp[u] + kb, c.k - kb - 16 * wc);
+                    g.w[u] = wp[u].part_raw(kb, c.k - kb - 16 * wc);
 #pragma unroll
                 for (int u = 0; u < LX; ++u)
-                    g.x[u] = load16_part(xp[u] + 2 * kb, 2 * (c.k - kb - 8 * xc));
+                    g.x[u] = xp[u].part_raw(2 * kb, 2 * (c.k - kb - 8 * xc));
             }
         };
         auto put = [&](const Regs& g, int b) {
 #pragma unroll
             for (int u = 0; u < LW; ++u)
-                *reinterpret_cast<u32x4*>(&lds[b][wo[u]]) = g.w[u];
+                *reinterpret_cast<u32x4*>(&lds[b][wo[u]]) = wp[u].bytes(g.w[u]);
 #pragma unroll
             for (int u = 0; u < LX; ++u)
-                *reinterpret_cast<u32x4*>(&lds[b][xo[u]]) = g.x[u];
+                *reinterpret_cast<u32x4*>(&lds[b][xo[u]]) = xp[u].bytes(g.x[u]);
         };
         auto compute = [&](int b) {
 #pragma unroll
@@ -609,12 +613,22 @@ ExpertPlan experts_plan(int64_t m, int64_t e, int64_t n, int64_t k, int64_t xr, 
     return {ExpertKind::TILE, 64, 64, 4};
 }
 
+// Whether some row starts below dword alignment.
+bool shifted(const ExpertCall& c)
+{
+    return ((reinterpret_cast<uintptr_t>(c.x) | reinterpret_cast<uintptr_t>(c.q) | (uintptr_t)c.k) & 3) != 0;
+}
+
 template <typename A, int CT, int W>
 hipError_t run_stream(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + 16 * CT - 1) / (16 * CT), groups = TN * max_row_tiles(c.m, c.e, 16);
-    hipLaunchKernelGGL((experts_stream_kernel<A, CT, W>), dim3((unsigned)groups), dim3(W * kWave), 0, stream, c,
-                       (int)TN);
+    if (shifted(c))
+        hipLaunchKernelGGL((experts_stream_kernel<A, CT, W, true>), dim3((unsigned)groups), dim3(W * kWave), 0,
+                           stream, c, (int)TN);
+    else
+        hipLaunchKernelGGL((experts_stream_kernel<A, CT, W, false>), dim3((unsigned)groups), dim3(W * kWave), 0,
+                           stream, c, (int)TN);
     return hipGetLastError();
 }
 
@@ -622,8 +636,12 @@ template <typename A, int BN, int BM, int WN, int WM>
 hipError_t run_tile(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + BN - 1) / BN, groups = TN * max_row_tiles(c.m, c.e, BM);
-    hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM>), dim3((unsigned)groups), dim3(WN * WM * kWave), 0,
-                       stream, c, (int)TN);
+    if (shifted(c))
+        hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM, true>), dim3((unsigned)groups),
+                           dim3(WN * WM * kWave), 0, stream, c, (int)TN);
+    else
+        hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM, false>), dim3((unsigned)groups),
+                           dim3(WN * WM * kWave), 0, stream, c, (int)TN);
     return hipGetLastError();
 }
 

@@ -140,24 +140,27 @@ __device__ __forceinline__ void put_codes(int8_t* q, int64_t off, int64_t kx, u3
 
 // 16-bit rows of up to 2048 CH values, one workgroup per row, read once: each
 // thread keeps CH runs of eight values.
-template <typename A, int CH>
+template <typename A, int CH, bool SHIFT>
 __global__ __launch_bounds__(256) void quantize_row_kernel(const uint16_t* __restrict__ x, int64_t k,
                                                            int8_t* __restrict__ q, int64_t kx,
                                                            float* __restrict__ scale)
 {
     __shared__ uint32_t part[4];
     const int64_t row = blockIdx.x;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(x + row * k);
+    const Row<SHIFT> src(x + row * k);
+    typename Row<SHIFT>::Raw raw[CH];
     u32x4 v[CH];
     uint32_t big = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const int64_t off = 8 * ((int64_t)threadIdx.x + 256 * c);
-        v[c] = load16_part(src + 2 * off, 2 * (k - off));
+        raw[c] = off + 8 <= k ? src.load(2 * off) : src.part_raw(2 * off, 2 * (k - off));
     }
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+        v[c] = src.bytes(raw[c]);
         big = max_bits(v[c], big);
+    }
     big = (big >> 16) > (big & 0xffffu) ? big >> 16 : big & 0xffffu;
     big = wave_max_u32(big);
     if ((threadIdx.x & 63) == 0)
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(256) void quantize_row_kernel(const uint16_t* __res
 template <typename A>
 __device__ __forceinline__ uint16_t finish(int acc, float sx, float sw, float bias)
 {
-    return A::from_f32(__builtin_fmaf((float)acc * sx, sw, bias));
+    return rounded<A>(__builtin_fmaf((float)acc * sx, sw, bias));
 }
 
 struct Int8Call {
@@ -210,7 +213,7 @@ constexpr int kFusedK = 16384;
 //
 // Any k and any alignment: whole blocks take unaligned 16-byte loads, the last
 // k % 128 a masked step.
-template <typename A, int RT, int CT, int W, int U, bool FUSED>
+template <typename A, int RT, int CT, int W, int U, bool FUSED, bool SHIFT>
 __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int TN, int TM)
 {
     static_assert(!FUSED || RT == 1, "one token");
@@ -219,22 +222,22 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
     __shared__ uint32_t row_max[W];
     int tn, tm;
     xcd_tile<8>(blockIdx.x, TN, TM, tn, tm);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)tn * (16 * CT), m0 = (int64_t)tm * (16 * RT);
-    const int8_t* wp[CT];
-    const int8_t* xp[RT];
+    Row<SHIFT> wp[CT], xp[RT];
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
         const int64_t ch = n0 + 16 * t + r < c.n ? n0 + 16 * t + r : c.n - 1;
-        wp[t] = c.qw + ch * c.k + 16 * g;
+        wp[t] = Row<SHIFT>(c.qw + ch * c.k + 16 * g);
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         const int64_t tok = m0 + 16 * t + r < c.m ? m0 + 16 * t + r : c.m - 1;
-        xp[t] = FUSED ? row + 16 * g : c.qx + tok * c.kx + 16 * g;
+        if constexpr (!FUSED)
+            xp[t] = Row<SHIFT>(c.qx + tok * c.kx + 16 * g);
     }
     struct Block {
-        u32x4 w[CT][2], x[FUSED ? 1 : RT][2];
+        typename Row<SHIFT>::Raw w[CT][2], x[FUSED ? 1 : RT][2];
     };
     auto load = [&](Block& b, int64_t i) {
         const int64_t kb = 128 * i;
@@ -242,11 +245,11 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int t = 0; t < CT; ++t)
-                b.w[t][h] = load16_any(wp[t] + kb + 64 * h);
+                b.w[t][h] = wp[t].load(kb + 64 * h);
             if constexpr (!FUSED) {
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    b.x[t][h] = load16_any(xp[t] + kb + 64 * h);
+                    b.x[t][h] = xp[t].load(kb + 64 * h);
             }
         }
     };
@@ -256,20 +259,25 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
         acc[t] = i32x4{0};
     auto compute = [&](const Block& b, int64_t i) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+            u32x4 w[CT];
+#pragma unroll
+            for (int u = 0; u < CT; ++u)
+                w[u] = wp[u].bytes(b.w[u][h]);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
                 u32x4 xv;
                 if constexpr (FUSED)
-                    xv = *reinterpret_cast<const u32x4*>(xp[0] + 128 * i + 64 * h);
+                    xv = *reinterpret_cast<const u32x4*>(row + 16 * g + 128 * i + 64 * h);
                 else
-                    xv = b.x[t][h];
+                    xv = xp[t].bytes(b.x[t][h]);
 #pragma unroll
                 for (int u = 0; u < CT; ++u)
                     acc[t * CT + u] =
-                        __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b.w[u][h]),
+                        __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w[u]),
                                                               __builtin_bit_cast(i32x4, xv), acc[t * CT + u], 0, 0, 0);
             }
+        }
     };
     // this wave's blocks: wave, wave + W, .. below k / 128
     const int64_t whole = c.k / 128, mine = whole > wave ? (whole - wave + W - 1) / W : 0;
@@ -337,10 +345,14 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
             u32x4 w[CT];
 #pragma unroll
             for (int u = 0; u < CT; ++u)
-                w[u] = load16_part(reinterpret_cast<const uint8_t*>(wp[u]) + kb + 64 * h, left);
+                w[u] = wp[u].part(kb + 64 * h, left);
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const u32x4 xv = load16_part(reinterpret_cast<const uint8_t*>(xp[t]) + kb + 64 * h, left);
+                u32x4 xv;
+                if constexpr (FUSED)
+                    xv = *reinterpret_cast<const u32x4*>(row + 16 * g + kb + 64 * h);  // zeros from k on
+                else
+                    xv = xp[t].part(kb + 64 * h, left);
 #pragma unroll
                 for (int u = 0; u < CT; ++u)
                     acc[t * CT + u] =
@@ -481,7 +493,7 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Call c, const int* _
 // every 64-byte row keeps its four 16-byte chunks rotated by row / 4, so the 16
 // lanes of a read's phase (16 rows, same chunk) hit distinct banks. Each XCD
 // starts its own eighth of k on.
-template <typename A, int BN, int BM, int WN, int WM>
+template <typename A, int BN, int BM, int WN, int WM, bool SHIFT>
 __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, int TN, int TM)
 {
     constexpr int NT = WN * WM * kWave, FN = BN / WN / 32, FM = BM / WM / 32;
@@ -495,7 +507,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
     __shared__ __attribute__((aligned(16))) float e_sx[BM];
     int tn, tm;
     xcd_tile<4>(blockIdx.x, TN, TM, tn, tm);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int i = lane & 31, h = lane >> 5, wn = wave % WN, wm = wave / WN;
     const int64_t n0 = (int64_t)tn * BN, m0 = (int64_t)tm * BM;
     if (tid < BN) {
@@ -505,51 +517,51 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
     }
     if (tid < BM)
         e_sx[tid] = c.sx[m0 + tid < c.m ? m0 + tid : c.m - 1];
-    const uint8_t *wp[LW], *xp[LX];
+    Row<SHIFT> wp[LW], xp[LX];
     int wo[LW], xo[LX];
     const int ch = tid & 3;
 #pragma unroll
     for (int u = 0; u < LW; ++u) {
         const int r = (tid >> 2) + NT / 4 * u;
-        wp[u] = reinterpret_cast<const uint8_t*>(c.qw) + (n0 + r < c.n ? n0 + r : c.n - 1) * c.k + 16 * ch;
+        wp[u] = Row<SHIFT>(c.qw + (n0 + r < c.n ? n0 + r : c.n - 1) * c.k + 16 * ch);
         wo[u] = 64 * r + 16 * ((ch + (r >> 2)) & 3);
     }
 #pragma unroll
     for (int u = 0; u < LX; ++u) {
         const int r = (tid >> 2) + NT / 4 * u;
-        xp[u] = reinterpret_cast<const uint8_t*>(c.qx) + (m0 + r < c.m ? m0 + r : c.m - 1) * c.kx + 16 * ch;
+        xp[u] = Row<SHIFT>(c.qx + (m0 + r < c.m ? m0 + r : c.m - 1) * c.kx + 16 * ch);
         xo[u] = 64 * r + 16 * ((ch + (r >> 2)) & 3);
     }
     const int64_t S = (c.k + 63) / 64, rot = (blockIdx.x % 8) * (S / 8);
     struct Regs {
-        u32x4 w[LW], x[LX];
+        typename Row<SHIFT>::Raw w[LW], x[LX];
     };
     auto load = [&](Regs& g, int64_t s) {
         const int64_t sr = s + rot < S ? s + rot : s + rot - S, kb = 64 * sr;
         if (kb + 64 <= c.k) {
 #pragma unroll
             for (int u = 0; u < LW; ++u)
-                g.w[u] = load16_any(wp[u] + kb);
+                g.w[u] = wp[u].load(kb);
 #pragma unroll
             for (int u = 0; u < LX; ++u)
-                g.x[u] = load16_any(xp[u] + kb);
+                g.x[u] = xp[u].load(kb);
         } else {
             const int64_t left = c.k - kb - 16 * ch;
 #pragma unroll
             for (int u = 0; u < LW; ++u)
-                g.w[u] = load16_part(wp[u] + kb, left);
+                g.w[u] = wp[u].part_raw(kb, left);
 #pragma unroll
             for (int u = 0; u < LX; ++u)
-                g.x[u] = load16_part(xp[u] + kb, left);
+                g.x[u] = xp[u].part_raw(kb, left);
         }
     };
     auto put = [&](const Regs& g, int b) {
 #pragma unroll
         for (int u = 0; u < LW; ++u)
-            *reinterpret_cast<u32x4*>(&lw[b][wo[u]]) = g.w[u];
+            *reinterpret_cast<u32x4*>(&lw[b][wo[u]]) = wp[u].bytes(g.w[u]);
 #pragma unroll
         for (int u = 0; u < LX; ++u)
-            *reinterpret_cast<u32x4*>(&lx[b][xo[u]]) = g.x[u];
+            *reinterpret_cast<u32x4*>(&lx[b][xo[u]]) = xp[u].bytes(g.x[u]);
     };
     i32x16 acc[FN * FM];
 #pragma unroll
@@ -814,19 +826,36 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int64_t kx, const int8_t* qw
     return tile_plan(Int8Kind::TILE, m, n, 64, 64, 1);
 }
 
+// Whether some row of codes starts below dword alignment.
+bool shifted(const Int8Call& c)
+{
+    return ((reinterpret_cast<uintptr_t>(c.qw) | reinterpret_cast<uintptr_t>(c.qx) | (uintptr_t)c.k |
+             (uintptr_t)c.kx) & 3) != 0;
+}
+
 template <typename A, int RT, int CT, int W, int U, bool FUSED>
 hipError_t run_stream(const Int8Call& c, const Int8Plan& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((int8_stream_kernel<A, RT, CT, W, U, FUSED>), dim3((unsigned)(p.TN * p.TM)), dim3(W * kWave), 0,
-                       stream, c, (int)p.TN, (int)p.TM);
+    const dim3 grid((unsigned)(p.TN * p.TM)), block(W * kWave);
+    if (shifted(c))
+        hipLaunchKernelGGL((int8_stream_kernel<A, RT, CT, W, U, FUSED, true>), grid, block, 0, stream, c, (int)p.TN,
+                           (int)p.TM);
+    else
+        hipLaunchKernelGGL((int8_stream_kernel<A, RT, CT, W, U, FUSED, false>), grid, block, 0, stream, c, (int)p.TN,
+                           (int)p.TM);
     return hipGetLastError();
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
 hipError_t run_tile(const Int8Call& c, const Int8Plan& p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM>), dim3((unsigned)(p.TN * p.TM)), dim3(WN * WM * kWave), 0,
-                       stream, c, (int)p.TN, (int)p.TM);
+    const dim3 grid((unsigned)(p.TN * p.TM)), block(WN * WM * kWave);
+    if (shifted(c))
+        hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, true>), grid, block, 0, stream, c, (int)p.TN,
+                           (int)p.TM);
+    else
+        hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, false>), grid, block, 0, stream, c, (int)p.TN,
+                           (int)p.TM);
     return hipGetLastError();
 }
 
@@ -901,16 +930,22 @@ template <typename A>
 void run_quantize(const void* x, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale, hipStream_t stream)
 {
     const uint16_t* src = static_cast<const uint16_t*>(x);
+    const bool shift = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(2 * k)) & 3) != 0;
+    const dim3 grid((unsigned)rows), block(256);
 #define FP8W_ROW(CH)                                                                                                   \
-    hipLaunchKernelGGL((quantize_row_kernel<A, CH>), dim3((unsigned)rows), dim3(256), 0, stream, src, k, q, kx, scale)
-    if (kx <= 2048)
+    if (shift)                                                                                                         \
+        hipLaunchKernelGGL((quantize_row_kernel<A, CH, true>), grid, block, 0, stream, src, k, q, kx, scale);          \
+    else                                                                                                               \
+        hipLaunchKernelGGL((quantize_row_kernel<A, CH, false>), grid, block, 0, stream, src, k, q, kx, scale)
+    if (kx <= 2048) {
         FP8W_ROW(1);
-    else if (kx <= 4096)
+    } else if (kx <= 4096) {
         FP8W_ROW(2);
-    else if (kx <= 8192)
+    } else if (kx <= 8192) {
         FP8W_ROW(4);
-    else
+    } else {
         FP8W_ROW(8);
+    }
 #undef FP8W_ROW
 }
 
