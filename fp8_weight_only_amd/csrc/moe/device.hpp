@@ -31,17 +31,29 @@ __device__ __forceinline__ void store16_any(void* p, u32x4 v)
     *static_cast<u32x4_any*>(p) = v;
 }
 
-// The first `avail` of 16 bytes at p, zeros after them; reads no byte past them.
+// The first `avail` of 16 bytes at p, zeros after them. Reads whole aligned
+// dwords, and none that holds no byte of those.
 __device__ __forceinline__ u32x4 load16_part(const uint8_t* p, int64_t avail)
 {
     if (avail >= 16)
         return load16_any(p);
-    uint32_t w[4] = {0, 0, 0, 0};
+    u32x4 r{0, 0, 0, 0};
+    if (avail > 0) {
+        const uint32_t shift = (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u, n = (uint32_t)avail;
+        const uint32_t* d = reinterpret_cast<const uint32_t*>(p - shift);
+        const uint32_t last = (shift + n - 1) / 4;
+        uint32_t v[5], o[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < avail)
-            w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-    return u32x4{w[0], w[1], w[2], w[3]};
+        for (uint32_t i = 0; i < 5; ++i)
+            v[i] = d[i < last ? i : last];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            const uint32_t w = __builtin_amdgcn_alignbyte(v[i + 1], v[i], shift);
+            o[i] = n >= 4 * i + 4 ? w : (n > 4 * i ? w & ((1u << (8 * (n - 4 * i))) - 1) : 0);
+        }
+        r = u32x4{o[0], o[1], o[2], o[3]};
+    }
+    return r;
 }
 
 // The largest v of the wave, in every lane: DPP shifts within rows of 16 lanes,
