@@ -280,12 +280,18 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
         }
     };
     // this wave's blocks: wave, wave + W, .. below k / 128
-    const int64_t whole = c.k / 128, mine = whole > wave ? (whole - wave + W - 1) / W : 0;
+    const int whole = (int)(c.k / 128), mine = whole > wave ? (whole - wave + W - 1) / W : 0;
     Block buf[U];
+    if (mine >= U) {  // no branch between the first loads
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (u < mine)
-            load(buf[u], wave + (int64_t)u * W);
+        for (int u = 0; u < U; ++u)
+            load(buf[u], wave + u * W);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (u < mine)
+                load(buf[u], wave + u * W);
+    }
     float token_scale = 0.0f;
     if constexpr (FUSED) {
         constexpr int NT = W * kWave, CH = kFusedK / 8 / NT;
@@ -318,27 +324,34 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
         }
         __syncthreads();
     }
-    int64_t done = 0;
-    for (; done + 2 * U <= mine; done += U) {
+    if (mine >= U) {
+        int done = 0;
+        for (; done + 2 * U <= mine; done += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                compute(buf[u], wave + (done + u) * W);
+                load(buf[u], wave + (done + u + U) * W);
+            }
+        }
+        const int rest = mine - done - U;  // fewer than U
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             compute(buf[u], wave + (done + u) * W);
-            load(buf[u], wave + (done + u + U) * W);
+            if (u < rest)
+                load(buf[u], wave + (done + u + U) * W);
         }
-    }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (done + u < mine)
-            compute(buf[u], wave + (done + u) * W);
-        if (done + u + U < mine)
-            load(buf[u], wave + (done + u + U) * W);
-    }
+        for (int u = 0; u < U - 1; ++u)
+            if (u < rest)
+                compute(buf[u], wave + (done + u + U) * W);
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (done + u + U < mine)
-            compute(buf[u], wave + (done + u + U) * W);
-    const int64_t kb = 128 * whole;
-    if (kb < c.k && wave == (int)(whole % W)) {
+        for (int u = 0; u < U - 1; ++u)
+            if (u < mine)
+                compute(buf[u], wave + u * W);
+    }
+    const int64_t kb = 128 * (int64_t)whole;
+    if (kb < c.k && wave == whole % W) {
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             const int64_t left = c.k - kb - 64 * h - 16 * g;
