@@ -158,11 +158,9 @@ fp8w_status_t fp8w_combine(const void* y, fp8w_dtype_t act_dtype, const float* w
     return hip_status(fp8w::launch_combine(y, act_of(act_dtype), weights, t, top_k, n, out, stream));
 }
 
-size_t fp8w_linear_experts_workspace_bytes(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q)
+size_t fp8w_linear_experts_workspace_bytes(int64_t, int64_t, int64_t, int64_t, const void*, const uint8_t*)
 {
-    if (!expert_sizes_ok(m, e, n, k))
-        return 0;
-    return m > 0 && n > 0 ? fp8w::experts_workspace_bytes(m, e, n, k, x, q) : 0;
+    return 0;  // k is split over the waves of a workgroup, or not at all
 }
 
 const char* fp8w_linear_experts_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q)
@@ -174,8 +172,8 @@ const char* fp8w_linear_experts_kernel(int64_t m, int64_t e, int64_t n, int64_t 
 
 fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype, int64_t x_count, int64_t k, const uint8_t* q,
                                   const float* scale, const void* bias, int64_t e, int64_t n, const int32_t* offsets,
-                                  int64_t m, const int32_t* x_rows, const int32_t* y_rows, void* y, void* workspace,
-                                  size_t workspace_bytes, hipStream_t stream)
+                                  int64_t m, const int32_t* x_rows, const int32_t* y_rows, void* y, void*, size_t,
+                                  hipStream_t stream)
 {
     if (!valid_act(act_dtype) || !dim_ok(x_count) || !expert_sizes_ok(m, e, n, k) || !product_ok(x_count, k))
         return FP8W_ERR_INVALID_VALUE;
@@ -198,17 +196,8 @@ fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype, int64_t
     const Span out{y, (size_t)m * (size_t)n * 2};
     if (overlaps_any(out, in))
         return FP8W_ERR_INVALID_VALUE;
-    const size_t need = fp8w::experts_workspace_bytes(m, e, n, k, x, q);
-    const bool use_ws = need > 0 && workspace && workspace_bytes >= need;
-    if (use_ws) {
-        if (!aligned(workspace, 16))
-            return FP8W_ERR_MISALIGNED;
-        if (overlaps_any({workspace, need}, in) || overlap({workspace, need}, out))
-            return FP8W_ERR_INVALID_VALUE;
-    }
     const fp8w::ExpertCall c{x, x_count, k, q, scale, bias, e, n, offsets, m, x_rows, y_rows, y};
-    return hip_status(
-        fp8w::launch_experts(c, act_of(act_dtype), use_ws ? workspace : nullptr, use_ws ? need : 0, stream));
+    return hip_status(fp8w::launch_experts(c, act_of(act_dtype), stream));
 }
 
 fp8w_status_t fp8w_quantize_int8(const void* w, fp8w_dtype_t w_dtype, int64_t n, int64_t k, int8_t* q, float* scale,

@@ -63,8 +63,15 @@ __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos,
 // both operands agree. The next block's loads are in flight during a block's
 // products. The waves' sums meet in LDS and are added in wave order.
 //
-// Any k and any alignment: whole blocks take unaligned 16-byte loads, the last
-// k % 128 a masked step.
+// Any k and any alignment: whole blocks take 16-byte loads from any dword (below
+// that, Row), the last k % 128 a masked step.
+//
+// Bound by the weight stream: one token, two of eight [14336, 4096] experts read
+// 117 MB in 22 us on 448 workgroups of eight waves, 5.3 TB/s, where a large copy
+// reaches 5.2. Measured against it: four waves the same; 32 or 16 channels per
+// workgroup 23 to 25 us (more waves load the same activations); four blocks per
+// wave in flight 26, for fewer waves per CU; loads that bypass the caches 27 to
+// 30 (two lanes' 64-byte halves of a line come by separate instructions).
 template <typename A, int CT, int W, bool SHIFT>
 __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, int TN)
 {
@@ -174,6 +181,13 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
 // their eight chunks rotated by row / 2, so the 16 lanes of a read's phase (16
 // rows, same chunk) hit distinct banks. The codes are decoded on their way from
 // LDS to the matrix cores: every e4m3 value is a bf16 and an fp16 value.
+//
+// Two waves per SIMD and 256 x 256 tiles (128 x 64 per wave) where the rows fill
+// them: 4096 tokens, two of eight [14336, 4096] experts take 870 us, 1.1 PFLOP/s
+// with the matrix cores busy 64 % of the time at a clock of 1.94 GHz and no bank
+// conflicts; a large bf16 product of the vendor's library runs at 1.3 PFLOP/s
+// there. Raised wave priority around the products, another grouping of tiles per
+// XCD (2, 8) and no stagger of k measured the same within 2 %.
 //
 // A half of a stage is 32 k: lane (i, h) takes the 16 codes and the 16 values at
 // k = 16 h of its rows, eight for each of two v_mfma_f32_32x32x16. Which k meet
@@ -686,12 +700,7 @@ hipError_t launch_typed(const ExpertCall& c, hipStream_t stream)
 
 }  // namespace
 
-size_t experts_workspace_bytes(int64_t, int64_t, int64_t, int64_t, const void*, const uint8_t*)
-{
-    return 0;
-}
-
-hipError_t launch_experts(const ExpertCall& c, Act act, void*, size_t, hipStream_t stream)
+hipError_t launch_experts(const ExpertCall& c, Act act, hipStream_t stream)
 {
     return act == Act::BF16 ? launch_typed<Bf16>(c, stream) : launch_typed<F16>(c, stream);
 }

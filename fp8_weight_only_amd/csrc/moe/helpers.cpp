@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -75,6 +76,9 @@ PyObject* none()
     Py_RETURN_NONE;
 }
 
+// The launches and allocations of a call go to its first tensor's device.
+#define FP8W_ON_DEVICE_OF(arg) const c10::DeviceGuard on_device((arg).t->device())
+
 // Runs f, and turns a C++ exception into a Python one.
 template <typename F>
 PyObject* guarded(F&& f)
@@ -110,6 +114,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int64_t t = w.size(0), top = w.size(1), c = y.size(1);
         if (!y.like(y, y.type(), {t * top, c}) || !w.like(y, at::kFloat, {t, top}) || !out.like(y, y.type(), {t, c}))
             return none();
+        FP8W_ON_DEVICE_OF(y);
         const at::Tensor made = out.given ? *out.t : make(y, {t, c}, y.type());
         const hipStream_t stream = stream_of(y);
         const fp8w_status_t st = without_gil([&] {
@@ -139,6 +144,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (renorm < 0 || (dt == FP8W_FP32 && type != at::kFloat) || top < 1 || top > e || top > 64 || e > 1024 ||
             t > INT32_MAX / top)
             return none();
+        FP8W_ON_DEVICE_OF(l);
         // one allocation: weights, experts, slots, tokens, offsets, workspace
         const int64_t s = t * top;
         const size_t need = fp8w_route_workspace_bytes(t, e, top);
@@ -184,6 +190,7 @@ PyObject* linear_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
             return none();
         const uint8_t* qp = static_cast<const uint8_t*>(q.ptr());
         const size_t need = fp8w_linear_experts_workspace_bytes(m, e, c, k, x.ptr(), qp);
+        FP8W_ON_DEVICE_OF(x);
         const at::Tensor made = out.given ? *out.t : make(x, {m, c}, x.type());
         at::Tensor ws;
         if (need)
@@ -216,6 +223,7 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
             return none();
         const int8_t* qp = static_cast<const int8_t*>(q.ptr());
         const size_t need = fp8w_linear_int8_workspace_bytes(m, c, k, x.ptr(), qp);
+        FP8W_ON_DEVICE_OF(x);
         const at::Tensor made = out.given ? *out.t : make(x, {m, c}, x.type());
         at::Tensor ws;
         if (need)

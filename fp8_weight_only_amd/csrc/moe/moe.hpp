@@ -59,8 +59,7 @@ struct ExpertCall {
     const int32_t *x_rows, *y_rows;
     void* y;
 };
-size_t experts_workspace_bytes(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q);
-hipError_t launch_experts(const ExpertCall& c, Act act, void* ws, size_t ws_bytes, hipStream_t stream);
+hipError_t launch_experts(const ExpertCall& c, Act act, hipStream_t stream);
 const char* experts_kernel_name(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q);
 
 // qx rows are kx >= k bytes apart (kx > k: bytes k .. kx - 1 of every row are

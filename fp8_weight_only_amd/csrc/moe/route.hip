@@ -27,6 +27,12 @@
 // slots: every wave owns a run of the chunk's slots and ranks 64 at a time by
 // the lanes that hold the same expert. Few tokens are one chunk: one workgroup
 // does all of it in a single launch.
+//
+// 32768 tokens, 8 of 256 experts, fp32: 24 us for the choice and 10 for the
+// order, where the logits alone take 7 at the rate of a large copy. The choice is
+// bound by vector instructions (one more choice of 32768 costs 1.9 us; with one,
+// 11), the order by its chain of short steps (8 us for 4096 tokens). One token, 8
+// of 128: 5.7 us in its launch.
 #include <math.h>
 
 #include "device.hpp"

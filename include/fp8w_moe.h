@@ -63,10 +63,10 @@ FP8W_API size_t fp8w_route_workspace_bytes(int64_t t, int64_t e, int64_t top_k);
  *   x_rows, y_rows  [m] int32 on the device, or NULL; dst(p) = y_rows[p], or p.
  *            y_rows must not name a row twice.
  *   y        [m, n] of act_dtype; must not overlap an input.
- *   workspace of fp8w_linear_experts_workspace_bytes bytes (16-byte aligned)
- *            where that is not 0; with less, a slower plan runs.
+ *   workspace, workspace_bytes: not used by the present plans.
  * Device values are not validated, and nothing outside the buffers is touched
- * whatever they hold: offsets are clamped to 0 .. m, a position whose src is
+ * whatever they hold (but for the rest of an aligned dword, which is read with a
+ * byte of it): offsets are clamped to 0 .. m, a position whose src is
  * outside x gives a row of NaN, one whose dst is outside y is not written.
  */
 FP8W_API fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype, int64_t x_count, int64_t k,
@@ -75,13 +75,11 @@ FP8W_API fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype
                                            const int32_t* y_rows, void* y, void* workspace, size_t workspace_bytes,
                                            hipStream_t stream);
 
-/* Workspace bytes fp8w_linear_experts uses for these sizes and pointers (NULL:
- * aligned); 0 where it uses none or the sizes are invalid. */
+/* Workspace bytes fp8w_linear_experts uses: 0 in this version. */
 FP8W_API size_t fp8w_linear_experts_workspace_bytes(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                     const uint8_t* q);
 
-/* Name of the kernel fp8w_linear_experts runs for an x of up to m rows (with its
- * workspace), NULL for invalid sizes and calls that run none. The string lives until the thread's
+/* Name of the kernel fp8w_linear_experts runs for an x of up to m rows, NULL for invalid sizes and calls that run none. The string lives until the thread's
  * next call. */
 FP8W_API const char* fp8w_linear_experts_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                 const uint8_t* q);
