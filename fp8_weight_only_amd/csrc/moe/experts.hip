@@ -344,8 +344,7 @@ __device__ __forceinline__ bool find_tile(const ExpertCall& c, int TN, int& tn, 
 }
 
 // Any k, any alignment, any number of rows in x: a stage passes through
-// registers into LDS. Stage s + 2 is requested when stage s begins, stage s + 1
-// is written to the other LDS buffer when it ends.
+// registers into LDS (run_tile_staged).
 template <typename A, int BN, int BM, int WN, int WM, bool SHIFT>
 __global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall c, int TN)
 {
@@ -390,15 +389,19 @@ __global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall 
         struct Regs {
             typename Row<SHIFT>::Raw w[LW], x[LX];
         };
-        auto load = [&](Regs& g, int64_t s) {
-            const int64_t kb = 64 * s;
+        auto load_whole = [&](Regs& g, int s) {
+            const int64_t kb = 64 * (int64_t)s;
+#pragma unroll
+            for (int u = 0; u < LW; ++u)
+                g.w[u] = wp[u].load(kb);
+#pragma unroll
+            for (int u = 0; u < LX; ++u)
+                g.x[u] = xp[u].load(2 * kb);
+        };
+        auto load = [&](Regs& g, int s) {
+            const int64_t kb = 64 * (int64_t)s;
             if (kb + 64 <= c.k) {
-#pragma unroll
-                for (int u = 0; u < LW; ++u)
-                    g.w[u] = wp[u].load(kb);
-#pragma unroll
-                for (int u = 0; u < LX; ++u)
-                    g.x[u] = xp[u].load(2 * kb);
+                load_whole(g, s);
             } else {
 #pragma unroll
                 for (int u = 0; u < LW; ++u)
@@ -424,28 +427,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void experts_tile_kernel(ExpertCall 
                 p.mma(f, acc);
             }
         };
-        Regs r0, r1;
-        load(r0, 0);
-        if (S > 1)
-            load(r1, 1);
-        put(r0, 0);
-        __syncthreads();
-        for (int64_t s = 0; s < S; s += 2) {
-            if (s + 2 < S)
-                load(r0, s + 2);
-            compute(0);
-            if (s + 1 < S)
-                put(r1, 1);
-            __syncthreads();
-            if (s + 1 < S) {
-                if (s + 3 < S)
-                    load(r1, s + 3);
-                compute(1);
-                if (s + 2 < S)
-                    put(r0, 0);
-                __syncthreads();
-            }
-        }
+        run_tile_staged<Regs>((int)S, (int)(c.k / 64), load, load_whole, put, compute);
     } else {
         __syncthreads();
     }
@@ -569,7 +551,7 @@ constexpr ExpertPlan kRings[] = {{ExpertKind::RING, 256, 256, 8}, {ExpertKind::R
                                  {ExpertKind::RING, 256, 32, 4},  {ExpertKind::RING, 128, 32, 4},
                                  {ExpertKind::RING, 64, 32, 2}};
 constexpr ExpertPlan kTiles[] = {{ExpertKind::TILE, 256, 128, 8}, {ExpertKind::TILE, 128, 64, 4},
-                                 {ExpertKind::TILE, 64, 64, 4}};
+                                 {ExpertKind::TILE, 64, 64, 4}, {ExpertKind::TILE, 128, 32, 4}};
 
 // Stages of a ring's tile: what LDS holds.
 constexpr int ring_depth(int bn, int bm)
@@ -597,14 +579,21 @@ ExpertPlan stream_plan(int64_t active, int64_t n, int64_t k)
 // A tile's channels are halved while it leaves CUs idle; 128 x 32 where k is
 // short (several workgroups per CU then overlap their starts: 85 against 104 us
 // at k = 1024, 4 rows), 256 x 32 where it is long (89 against 96 at k = 4096).
-// Unaligned rows: the stream kernel up to 8 rows, then the tiles.
+// Layers too small for their tiles to fill the CUs: the stream kernel, whose
+// waves split k ([256, 14080] x 5, five rows each: 17 us against 35).
+// Rows that the ring cannot load, and k below 320 (its starts and ends are most
+// of it then): the register-staged tiles, 128 x 32 up to 16 rows ([4096, 1023] x
+// 128, four rows: 127 us; 128 x 64 169, the stream 171; but 23 rows, unevenly
+// spread, [1030, 1001] x 60: 33 against 27), 128 x 64 up to 96 ([11904, 256] x 40,
+// 83 rows: 110 us; 256 x 128 123), 256 x 128 above.
 ExpertPlan experts_plan(int64_t m, int64_t e, int64_t n, int64_t k, int64_t xr, const void* x, const uint8_t* q)
 {
     const int64_t active = m < e ? m : e, rows = (m + active - 1) / active;
     const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-    const bool ring = aligned && k % 64 == 0 && k >= 256 && k <= (1 << 22) && xr <= ((int64_t)1 << 30) / k;
+    const bool ring = aligned && k % 64 == 0 && k >= 320 && k <= (1 << 22) && xr <= ((int64_t)1 << 30) / k;
     const ExpertPlan st = stream_plan(active, n, k);
-    if (rows <= (ring ? 2 : 8) && st.fits(m, e, n))
+    const bool streams = st.fits(m, e, n);
+    if (rows <= 2 && streams)
         return st;
     auto fills = [&](const ExpertPlan& p, int64_t least) {
         return (n + p.a - 1) / p.a * active * ((rows + p.b - 1) / p.b) >= least && p.fits(m, e, n);
@@ -617,12 +606,16 @@ ExpertPlan experts_plan(int64_t m, int64_t e, int64_t n, int64_t k, int64_t xr, 
             if (fills(p, p.b == 256 ? 128 : 224))
                 return p;
         }
-        for (const ExpertPlan& p : kRings)  // a small layer: the narrowest tile for these rows
-            if (p.a == 64 && p.b <= bm && p.fits(m, e, n))
+    } else {
+        const int bm = rows <= 16 ? 32 : (rows <= 96 ? 64 : 128);
+        for (const ExpertPlan& p : kTiles)
+            if (p.b <= bm && fills(p, 224))
                 return p;
     }
-    for (const ExpertPlan& p : kTiles)
-        if (p.b <= (rows <= 64 ? 64 : 128) && fills(p, 224))
+    if (rows <= 64 && streams)
+        return st;
+    for (const ExpertPlan& p : kRings)
+        if (ring && p.a == 64 && p.b == 64 && p.fits(m, e, n))
             return p;
     return {ExpertKind::TILE, 64, 64, 4};
 }
@@ -683,6 +676,7 @@ hipError_t launch_typed(const ExpertCall& c, hipStream_t stream)
     }
     if (p.kind == ExpertKind::TILE)
         return p.a == 256   ? run_tile<A, 256, 128, 2, 4>(c, stream)
+               : p.b == 32  ? run_tile<A, 128, 32, 4, 1>(c, stream)
                : p.a == 128 ? run_tile<A, 128, 64, 2, 2>(c, stream)
                             : run_tile<A, 64, 64, 2, 2>(c, stream);
     if (p.b == 256)

@@ -510,11 +510,9 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Call c, const int* _
 
 // Many tokens (prefill): BN channels x BM tokens, WN x WM waves of 32 x 32
 // fragments, stages of 64 k. A stage passes through registers into LDS, so any
-// k and any alignment take the same code: stage s + 2 is requested when stage s
-// begins, stage s + 1 is written to the other LDS buffer when it ends. In LDS
-// every 64-byte row keeps its four 16-byte chunks rotated by row / 4, so the 16
-// lanes of a read's phase (16 rows, same chunk) hit distinct banks. Each XCD
-// starts its own eighth of k on.
+// k and any alignment take the same code (run_tile_staged). In LDS every 64-byte
+// row keeps its four 16-byte chunks rotated by row / 4, so the 16 lanes of a
+// read's phase (16 rows, same chunk) hit distinct banks.
 template <typename A, int BN, int BM, int WN, int WM, bool SHIFT>
 __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, int TN, int TM)
 {
@@ -554,21 +552,24 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
         xp[u] = Row<SHIFT>(c.qx + (m0 + r < c.m ? m0 + r : c.m - 1) * c.kx + 16 * ch);
         xo[u] = 64 * r + 16 * ((ch + (r >> 2)) & 3);
     }
-    const int64_t S = (c.k + 63) / 64, rot = (blockIdx.x % 8) * (S / 8);
+    const int S = (int)((c.k + 63) / 64);
     struct Regs {
         typename Row<SHIFT>::Raw w[LW], x[LX];
     };
-    auto load = [&](Regs& g, int64_t s) {
-        const int64_t sr = s + rot < S ? s + rot : s + rot - S, kb = 64 * sr;
+    auto load_whole = [&](Regs& g, int s) {
+        const int64_t kb = 64 * (int64_t)s;
+#pragma unroll
+        for (int u = 0; u < LW; ++u)
+            g.w[u] = wp[u].load(kb);
+#pragma unroll
+        for (int u = 0; u < LX; ++u)
+            g.x[u] = xp[u].load(kb);
+    };
+    auto load = [&](Regs& g, int s) {
+        const int64_t kb = 64 * (int64_t)s, left = c.k - kb - 16 * ch;
         if (kb + 64 <= c.k) {
-#pragma unroll
-            for (int u = 0; u < LW; ++u)
-                g.w[u] = wp[u].load(kb);
-#pragma unroll
-            for (int u = 0; u < LX; ++u)
-                g.x[u] = xp[u].load(kb);
+            load_whole(g, s);
         } else {
-            const int64_t left = c.k - kb - 16 * ch;
 #pragma unroll
             for (int u = 0; u < LW; ++u)
                 g.w[u] = wp[u].part_raw(kb, left);
@@ -612,28 +613,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
         }
     };
     if (S > 0) {
-        Regs r0, r1;
-        load(r0, 0);
-        if (S > 1)
-            load(r1, 1);
-        put(r0, 0);
-        __syncthreads();
-        for (int64_t s = 0; s < S; s += 2) {
-            if (s + 2 < S)
-                load(r0, s + 2);
-            compute(0);
-            if (s + 1 < S)
-                put(r1, 1);
-            __syncthreads();
-            if (s + 1 < S) {
-                if (s + 3 < S)
-                    load(r1, s + 3);
-                compute(1);
-                if (s + 2 < S)
-                    put(r0, 0);
-                __syncthreads();
-            }
-        }
+        run_tile_staged<Regs>((int)S, (int)(c.k / 64), load, load_whole, put, compute);
     } else {
         __syncthreads();
     }

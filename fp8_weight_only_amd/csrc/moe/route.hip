@@ -542,12 +542,14 @@ int lanes(int64_t e, int64_t top)
     return e <= 64 && top <= 16 ? 16 : 64;
 }
 
-// One workgroup, one launch: up to two rounds of its waves. The two launches
-// take about 9 us however few the tokens; a round of one workgroup adds 2 to 4
-// (100 tokens, top 8 of 128, in four rounds: 18.4 us against 10.2).
+// One workgroup, one launch: one round of its waves, or few choices. The two
+// launches take 9 to 11 us however few the tokens; a round of one workgroup adds
+// about 0.35 us per choice (235 tokens, 6 of 44, in two rounds: 14.8 us against
+// 11.0; 250 tokens, 2 of 8: 7.4 against 9.3).
 bool small(int64_t t, int64_t e, int64_t top)
 {
-    return t * lanes(e, top) <= 4 * kThreads && t * top <= kSmallSlots;
+    const int64_t rounds = (t * lanes(e, top) + 2 * kThreads - 1) / (2 * kThreads);
+    return t * top <= kSmallSlots && (rounds <= 1 || rounds * (top + 2) <= 8);
 }
 
 template <int G, int J>

@@ -17,23 +17,28 @@ TINY = {BF: 2.0 ** -134, HF: 2.0 ** -25}
 EXPERTS = [
     # m, e, n, k, kernel
     (1200, 4, 4096, 320, "experts_ring_kernel<BN=256,BM=256,W=8>"),
-    (1030, 3, 8000, 256, "experts_ring_kernel<BN=256,BM=256,W=8>"),
-    (800, 8, 7168, 256, "experts_ring_kernel<BN=256,BM=128,W=8>"),
+    (1030, 3, 8000, 320, "experts_ring_kernel<BN=256,BM=256,W=8>"),
+    (800, 8, 7168, 384, "experts_ring_kernel<BN=256,BM=128,W=8>"),
     (800, 8, 4096, 448, "experts_ring_kernel<BN=128,BM=128,W=8>"),
-    (240, 8, 7200, 256, "experts_ring_kernel<BN=256,BM=64,W=8>"),
+    (240, 8, 7200, 320, "experts_ring_kernel<BN=256,BM=64,W=8>"),
     (240, 8, 4000, 320, "experts_ring_kernel<BN=128,BM=64,W=4>"),
     (240, 8, 2000, 576, "experts_ring_kernel<BN=64,BM=64,W=4>"),
     (40, 8, 7168, 2048, "experts_ring_kernel<BN=256,BM=32,W=4>"),
     (40, 8, 4096, 512, "experts_ring_kernel<BN=128,BM=32,W=4>"),
-    (40, 8, 1000, 256, "experts_ring_kernel<BN=64,BM=32,W=2>"),
+    (40, 8, 2000, 448, "experts_ring_kernel<BN=64,BM=32,W=2>"),
     (900, 300, 520, 384, "experts_ring_kernel<BN=128,BM=32,W=4>"),
+    (200, 13, 5000, 256, "experts_tile_kernel<BN=128,BM=32,W=4>"),
+    (100, 7, 6000, 129, "experts_tile_kernel<BN=128,BM=32,W=4>"),
+    (500, 8, 4000, 998, "experts_tile_kernel<BN=128,BM=64,W=4>"),
     (800, 8, 7168, 257, "experts_tile_kernel<BN=256,BM=128,W=8>"),
-    (800, 8, 4000, 300, "experts_tile_kernel<BN=128,BM=64,W=4>"),
+    (560, 8, 3700, 300, "experts_tile_kernel<BN=128,BM=64,W=4>"),
     (800, 8, 1000, 77, "experts_tile_kernel<BN=64,BM=64,W=4>"),
     (3, 8, 512, 512, "experts_stream_kernel<CT=1,W=4>"),
     (3, 8, 512, 4096, "experts_stream_kernel<CT=1,W=8>"),
     (30, 16, 4096, 512, "experts_stream_kernel<CT=4,W=4>"),
     (2, 2, 14000, 2048, "experts_stream_kernel<CT=4,W=8>"),
+    (40, 8, 1000, 1001, "experts_stream_kernel<CT=2,W=4>"),
+    (300, 5, 256, 5000, "experts_stream_kernel<CT=1,W=8>"),
     (3, 4, 2000, 100, "experts_stream_kernel<CT=1,W=4>"),
     (2, 2, 5000, 3000, "experts_stream_kernel<CT=2,W=8>"),
 ]
