@@ -512,9 +512,10 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8Call c, const int* _
 // fragments, stages of 64 k. A stage passes through registers into LDS, so any
 // k and any alignment take the same code (run_tile_staged). In LDS every 64-byte
 // row keeps its four 16-byte chunks rotated by row / 4, so the 16 lanes of a
-// read's phase (16 rows, same chunk) hit distinct banks.
+// read's phase (16 rows, same chunk) hit distinct banks. part: k is split into
+// slices of `stages` stages, as for the ring below.
 template <typename A, int BN, int BM, int WN, int WM, bool SHIFT>
-__global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, int TN, int TM)
+__global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, int TN, int TM, int stages, int* part)
 {
     constexpr int NT = WN * WM * kWave, FN = BN / WN / 32, FM = BM / WM / 32;
     constexpr int LW = BN * 4 / NT, LX = BM * 4 / NT;  // 16-byte chunks per thread and stage
@@ -526,7 +527,10 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
     __shared__ __attribute__((aligned(16))) uint16_t e_bias[BN];
     __shared__ __attribute__((aligned(16))) float e_sx[BM];
     int tn, tm;
-    xcd_tile<4>(blockIdx.x, TN, TM, tn, tm);
+    const int slice = blockIdx.x / (TN * TM);
+    xcd_tile<4>(blockIdx.x - slice * (TN * TM), TN, TM, tn, tm);
+    // this workgroup's part of k
+    const int64_t k0 = (int64_t)slice * stages * 64, kl = c.k - k0 < (int64_t)stages * 64 ? c.k - k0 : (int64_t)stages * 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int i = lane & 31, h = lane >> 5, wn = wave % WN, wm = wave / WN;
     const int64_t n0 = (int64_t)tn * BN, m0 = (int64_t)tm * BM;
@@ -543,16 +547,16 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
 #pragma unroll
     for (int u = 0; u < LW; ++u) {
         const int r = (tid >> 2) + NT / 4 * u;
-        wp[u] = Row<SHIFT>(c.qw + (n0 + r < c.n ? n0 + r : c.n - 1) * c.k + 16 * ch);
+        wp[u] = Row<SHIFT>(c.qw + (n0 + r < c.n ? n0 + r : c.n - 1) * c.k + k0 + 16 * ch);
         wo[u] = 64 * r + 16 * ((ch + (r >> 2)) & 3);
     }
 #pragma unroll
     for (int u = 0; u < LX; ++u) {
         const int r = (tid >> 2) + NT / 4 * u;
-        xp[u] = Row<SHIFT>(c.qx + (m0 + r < c.m ? m0 + r : c.m - 1) * c.kx + 16 * ch);
+        xp[u] = Row<SHIFT>(c.qx + (m0 + r < c.m ? m0 + r : c.m - 1) * c.kx + k0 + 16 * ch);
         xo[u] = 64 * r + 16 * ((ch + (r >> 2)) & 3);
     }
-    const int S = (int)((c.k + 63) / 64);
+    const int S = (int)((kl + 63) / 64);
     struct Regs {
         typename Row<SHIFT>::Raw w[LW], x[LX];
     };
@@ -566,8 +570,8 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
             g.x[u] = xp[u].load(kb);
     };
     auto load = [&](Regs& g, int s) {
-        const int64_t kb = 64 * (int64_t)s, left = c.k - kb - 16 * ch;
-        if (kb + 64 <= c.k) {
+        const int64_t kb = 64 * (int64_t)s, left = kl - kb - 16 * ch;
+        if (kb + 64 <= kl) {
             load_whole(g, s);
         } else {
 #pragma unroll
@@ -613,11 +617,14 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
         }
     };
     if (S > 0) {
-        run_tile_staged<Regs>((int)S, (int)(c.k / 64), load, load_whole, put, compute);
+        run_tile_staged<Regs>(S, (int)(kl / 64), load, load_whole, put, compute);
     } else {
         __syncthreads();
     }
-    store_tile<A, BN, BM, WN, WM>(c, n0, m0, wn, wm, lane, e_sw, e_bias, e_sx, acc);
+    if (part)
+        store_sums<BN, BM, WN, WM>(c, part + (int64_t)slice * c.m * c.n, n0, m0, wn, wm, lane, acc);
+    else
+        store_tile<A, BN, BM, WN, WM>(c, n0, m0, wn, wm, lane, e_sw, e_bias, e_sx, acc);
 }
 
 // More tokens, weight rows at 16-byte boundaries, k a multiple of 64: the same
@@ -831,7 +838,11 @@ Int8Plan int8_plan(int64_t m, int64_t n, int64_t k, int64_t kx, const int8_t* qw
         if (p.TN * p.TM >= 224)
             return p;
     }
-    return tile_plan(Int8Kind::TILE, m, n, 64, 64, 1);
+    p = tile_plan(Int8Kind::TILE, m, n, 64, 64, 1);
+    // few tiles and a long k: slices of eight stages or more (428 tokens, [256, 12149], 28 tiles: 71 us in one piece)
+    while (split && p.slices < 8 && p.TN * p.TM * p.slices < 128 && (k + 63) / 64 >= 16 * p.slices)
+        p.slices *= 2;
+    return p;
 }
 
 // Whether some row of codes starts below dword alignment.
@@ -854,17 +865,32 @@ hipError_t run_stream(const Int8Call& c, const Int8Plan& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <typename A, int BN, int BM, int WN, int WM>
-hipError_t run_tile(const Int8Call& c, const Int8Plan& p, hipStream_t stream)
+// Joins the slices of a k split.
+template <typename A>
+hipError_t join(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(p.TN * p.TM)), block(WN * WM * kWave);
+    const hipError_t st = hipGetLastError();
+    if (st != hipSuccess || p.slices == 1)
+        return st;
+    const int64_t items = c.m * ((c.n + 3) / 4);
+    hipLaunchKernelGGL(int8_join_kernel<A>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream, c, part,
+                       p.slices);
+    return hipGetLastError();
+}
+
+template <typename A, int BN, int BM, int WN, int WM>
+hipError_t run_tile(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(p.TN * p.TM * p.slices)), block(WN * WM * kWave);
+    const int stages = (int)(((c.k + 63) / 64 + p.slices - 1) / p.slices);
+    int* sums = p.slices > 1 ? part : nullptr;
     if (shifted(c))
         hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, true>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM);
+                           (int)p.TM, stages, sums);
     else
         hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, false>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM);
-    return hipGetLastError();
+                           (int)p.TM, stages, sums);
+    return join<A>(c, p, part, stream);
 }
 
 template <typename A, int BN, int BM, int WN, int WM, int NS>
@@ -873,13 +899,7 @@ hipError_t run_ring(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t
     hipLaunchKernelGGL((int8_ring_kernel<A, BN, BM, WN, WM, NS>), dim3((unsigned)(p.TN * p.TM * p.slices)),
                        dim3(WN * WM * kWave), 0, stream, c, (int)p.TN, (int)p.TM, (int)(c.k / 64 / p.slices),
                        p.slices > 1 ? part : nullptr);
-    const hipError_t st = hipGetLastError();
-    if (st != hipSuccess || p.slices == 1)
-        return st;
-    const int64_t items = c.m * ((c.n + 3) / 4);
-    hipLaunchKernelGGL(int8_join_kernel<A>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream, c, part,
-                       p.slices);
-    return hipGetLastError();
+    return join<A>(c, p, part, stream);
 }
 
 template <typename A>
@@ -896,8 +916,8 @@ hipError_t run_plan(const Int8Call& c, const Int8Plan& p, bool fuse, int* part, 
     }
     if (p.kind == Int8Kind::TILE) {
         if (p.a == 256)
-            return p.b == 256 ? run_tile<A, 256, 256, 2, 4>(c, p, stream) : run_tile<A, 256, 128, 2, 4>(c, p, stream);
-        return p.a == 128 ? run_tile<A, 128, 128, 2, 4>(c, p, stream) : run_tile<A, 64, 64, 2, 2>(c, p, stream);
+            return p.b == 256 ? run_tile<A, 256, 256, 2, 4>(c, p, part, stream) : run_tile<A, 256, 128, 2, 4>(c, p, part, stream);
+        return p.a == 128 ? run_tile<A, 128, 128, 2, 4>(c, p, part, stream) : run_tile<A, 64, 64, 2, 2>(c, p, part, stream);
     }
     if (fuse)
         return p.w == 8 ? run_stream<A, 1, 1, 8, 4, true>(c, p, stream)
@@ -1046,14 +1066,16 @@ const char* linear_int8_kernel_name(int64_t m, int64_t n, int64_t k, const void*
     const char* first = padded_k(k) > 16384 ? "quantize_int8_kernel" : "quantize_row_kernel";
     if (p.kind == Int8Kind::STREAM)
         snprintf(name, sizeof name, "%s+int8_stream_kernel<RT=%d,CT=%d,W=%d>", first, p.a, p.b, p.w);
-    else if (p.kind == Int8Kind::TILE)
-        snprintf(name, sizeof name, "%s+int8_tile_kernel<BN=%d,BM=%d,W=%d>", first, p.a, p.b, p.w);
-    else if (p.slices == 1)
-        snprintf(name, sizeof name, "%s+int8_ring_kernel<BN=%d,BM=%d,W=%d,NS=%d>", first, p.a, p.b, p.w,
-                 ring_depth(p.a));
-    else
-        snprintf(name, sizeof name, "%s+int8_ring_kernel<BN=%d,BM=%d,W=%d,NS=%d>*%d+int8_join_kernel", first, p.a,
-                 p.b, p.w, ring_depth(p.a), p.slices);
+    else {
+        char slices[32] = "";
+        if (p.slices > 1)
+            snprintf(slices, sizeof slices, "*%d+int8_join_kernel", p.slices);
+        if (p.kind == Int8Kind::TILE)
+            snprintf(name, sizeof name, "%s+int8_tile_kernel<BN=%d,BM=%d,W=%d>%s", first, p.a, p.b, p.w, slices);
+        else
+            snprintf(name, sizeof name, "%s+int8_ring_kernel<BN=%d,BM=%d,W=%d,NS=%d>%s", first, p.a, p.b, p.w,
+                     ring_depth(p.a), slices);
+    }
     return name;
 }
 

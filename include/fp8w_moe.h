@@ -8,7 +8,8 @@
  * validated before anything is enqueued, status codes and dtypes of fp8w.h.
  * Every call is asynchronous and can be captured into a HIP graph, but for
  * fp8w_quantize_int8, which synchronizes. A call's results depend on its
- * arguments alone (no order of atomics enters them). Sizes up to 2^31 - 1
+ * arguments alone (no order of atomics enters them). Inputs may be read by whole
+ * aligned dwords, that is with up to three bytes beside their first and last. Sizes up to 2^31 - 1
  * unless stated; a call that would need a launch of 2^32 threads or more (some
  * 6e10 outputs) is invalid.
  */
@@ -38,7 +39,8 @@ extern "C" {
  *   slots    [t * top_k] int32: the slots token * top_k + j by expert, rising
  *            within an expert; slots without an expert from offsets[e] on.
  *   tokens   [t * top_k] int32: slots / top_k.
- *   workspace of fp8w_route_workspace_bytes bytes, 4-byte aligned.
+ *   workspace of fp8w_route_workspace_bytes bytes (0 for few tokens), 4-byte
+ *            aligned.
  * No two buffers may overlap. t == 0 writes offsets (zeros).
  */
 FP8W_API fp8w_status_t fp8w_route(const void* logits, fp8w_dtype_t dtype, int64_t t, int64_t e, int64_t top_k,
@@ -65,8 +67,7 @@ FP8W_API size_t fp8w_route_workspace_bytes(int64_t t, int64_t e, int64_t top_k);
  *   y        [m, n] of act_dtype; must not overlap an input.
  *   workspace, workspace_bytes: not used by the present plans.
  * Device values are not validated, and nothing outside the buffers is touched
- * whatever they hold (but for the rest of an aligned dword, which is read with a
- * byte of it): offsets are clamped to 0 .. m, a position whose src is
+ * whatever they hold: offsets are clamped to 0 .. m, a position whose src is
  * outside x gives a row of NaN, one whose dst is outside y is not written.
  */
 FP8W_API fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype, int64_t x_count, int64_t k,

@@ -63,7 +63,9 @@ INT8 = [
     (3000, 6000, 300, "int8_tile_kernel<BN=256,BM=256,W=8>"),
     (1500, 6000, 100, "int8_tile_kernel<BN=256,BM=128,W=8>"),
     (700, 6000, 100, "int8_tile_kernel<BN=128,BM=128,W=8>"),
-    (300, 1030, 1001, "int8_tile_kernel<BN=64,BM=64,W=4>"),
+    (500, 1030, 1001, "int8_tile_kernel<BN=64,BM=64,W=4>"),
+    (200, 250, 1999, "int8_tile_kernel<BN=64,BM=64,W=4>*4+int8_join_kernel"),
+    (70, 300, 8198, "int8_tile_kernel<BN=64,BM=64,W=4>*8+int8_join_kernel"),
     (1, 1000, 1000, "int8_stream_kernel<RT=1,CT=1,W=4,FUSED>"),
     (1, 999, 16384, "int8_stream_kernel<RT=1,CT=1,W=8,FUSED>"),
     (1, 100, 20000, "int8_stream_kernel<RT=1,CT=1,W=8>"),
