@@ -183,7 +183,7 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
 // LDS to the matrix cores: every e4m3 value is a bf16 and an fp16 value.
 //
 // Two waves per SIMD and 256 x 256 tiles (128 x 64 per wave) where the rows fill
-// them: 4096 tokens, two of eight [14336, 4096] experts take 870 us, 1.1 PFLOP/s
+// them: 4096 tokens, two of eight [14336, 4096] experts take 849 us, 1.1 PFLOP/s
 // with the matrix cores busy 64 % of the time at a clock of 1.94 GHz and no bank
 // conflicts; a large bf16 product of the vendor's library runs at 1.3 PFLOP/s
 // there. Raised wave priority around the products, another grouping of tiles per

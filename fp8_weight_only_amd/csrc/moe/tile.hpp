@@ -106,6 +106,8 @@ __device__ __forceinline__ void run_tile_ring(const P& p, int S, const Buf& buf,
     static_assert(NS >= 2 && LOADS * (NS - 1) < 64, "vmcnt range");
     typename P::Frags f0, f1;
     auto at = [&](auto i) { return buf(std::integral_constant<int, decltype(i)::value % NS>{}); };
+    // A half's reads are issued before the products of the other (scheduling barriers); behind
+    // those the order is the compiler's, which measured 1 to 2 % faster than holding it too.
     // stage s (step u of a group of NS): `left` later stages may stay in flight
     // at the barrier (-1: this is the last stage), `more` says that stage s + NS exists
     auto step = [&](int s, auto uc, auto left, auto more) {
@@ -113,7 +115,6 @@ __device__ __forceinline__ void run_tile_ring(const P& p, int S, const Buf& buf,
         p.read(at(uc), 1, f1);
         __builtin_amdgcn_sched_barrier(0);
         p.mma(f0, acc);
-        __builtin_amdgcn_sched_barrier(0);
         if constexpr (decltype(left)::value >= 0) {
             wait_loads_at_most<LOADS * decltype(left)::value>();
             stage_barrier();
@@ -123,7 +124,6 @@ __device__ __forceinline__ void run_tile_ring(const P& p, int S, const Buf& buf,
             __builtin_amdgcn_sched_barrier(0);
         }
         p.mma(f1, acc);
-        __builtin_amdgcn_sched_barrier(0);
     };
     ring_for<0, NS>([&](auto i) { p.issue(decltype(i)::value, at(i)); });
     wait_loads_at_most<LOADS*(NS - 1)>();
