@@ -2,8 +2,9 @@
 // channel:
 //   sx[t] = max_k |x[t, k]| / 127,  qx[t, k] = round(127 x[t, k] / max_k |x[t, k]|)
 //   y[t, c] = (sum_k qx[t, k] * q[c, k]) * sx[t] * sw[c] + bias[c]
-// The sum is exact in 32-bit integers (k <= 131072), in whatever order; the
-// scales and the bias are applied in fp32 and the result is rounded once.
+// The sum is exact in 32-bit integers (k <= 131072), in whatever order (its one
+// value of 2^31: see sum_f32); the scales and the bias are applied in fp32 and
+// the result is rounded once.
 //
 // Codes of 16-bit activations are the exact quotient's nearest integers, ties to
 // even. 127 x has at most 18 significant bits, so it is exact in fp32, and x and
@@ -181,10 +182,17 @@ __global__ __launch_bounds__(NT) void quantize_row_kernel(const uint16_t* __rest
 }
 
 // ------------------------------------------------------------------ products
+// A sum in fp32. -128 * -128 taken 131072 times is 2^31, which wraps to -2^31;
+// no other sum is there, the lowest being -128 * 127 * 131072.
+__device__ __forceinline__ float sum_f32(int acc)
+{
+    return acc == INT32_MIN ? 0x1p31f : (float)acc;
+}
+
 template <typename A>
 __device__ __forceinline__ uint16_t finish(int acc, float sx, float sw, float bias)
 {
-    return rounded<A>(__builtin_fmaf((float)acc * sx, sw, bias));
+    return rounded<A>(__builtin_fmaf(sum_f32(acc) * sx, sw, bias));
 }
 
 struct Int8Call {
@@ -389,14 +397,14 @@ __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int T
     __syncthreads();
     // lane (r, g) holds channels 4 g .. 4 g + 3 of token r
     for (int t = wave; t < RT * CT; t += W) {
-        i32x4 sum = part[0][t][lane];
+        u32x4 sum = __builtin_bit_cast(u32x4, part[0][t][lane]);  // unsigned: 2^31 may wrap
 #pragma unroll
         for (int w = 1; w < W; ++w)
-            sum += part[w][t][lane];
+            sum += __builtin_bit_cast(u32x4, part[w][t][lane]);
         const int64_t tok = m0 + 16 * (t / CT) + r, c0 = n0 + 16 * (t % CT) + 4 * g;
         if (tok < c.m && c0 < c.n) {
             const float st = FUSED ? token_scale : c.sx[tok];
-            const int v[4] = {sum.x, sum.y, sum.z, sum.w};
+            const int v[4] = {(int)sum.x, (int)sum.y, (int)sum.z, (int)sum.w};
             uint16_t o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

@@ -15,7 +15,7 @@ enum class Act { BF16 = 0, FP16 = 1, FP32 = 2 };
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 64;
-constexpr int64_t kMaxInt8K = 131072;  // 127 * 127 * k stays below 2^31
+constexpr int64_t kMaxInt8K = 131072;  // 128 * 128 * k is at most 2^31
 
 // A grid of this many workgroups of `threads` stays under the 2^32 threads a
 // launch can have.

@@ -114,8 +114,8 @@ FP8W_API fp8w_status_t fp8w_quantize_activations_int8(const void* x, fp8w_dtype_
 
 /*
  * y[t, c] = (sum_k qx[t, k] * q[c, k]) * sx[t] * scale[c] + bias[c]: the sum in
- * 32-bit integers (exact: k <= 131072), the rest in fp32, rounded once to
- * out_dtype (BF16 or FP16). bias [n] of out_dtype, or NULL; y must not overlap
+ * 32-bit integers (exact for codes -128 .. 127: k <= 131072), the rest in fp32,
+ * rounded once to out_dtype (BF16 or FP16). bias [n] of out_dtype, or NULL; y must not overlap
  * an input.
  */
 FP8W_API fp8w_status_t fp8w_gemm_int8(const int8_t* qx, const float* sx, int64_t m, int64_t k, const int8_t* q,
