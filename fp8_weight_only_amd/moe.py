@@ -4,7 +4,7 @@ A thin ctypes binding over ``libfp8w_moe.so`` (declared in
 ``include/fp8w_moe.h``), in the manner of the package's FP8 linear layer: the
 raw entry points keep the C names and take integers; the tensor helpers check
 their arguments, allocate outputs and workspaces with torch and run on torch's
-current stream. The helpers of the timed path go through a small compiled module
+current stream of the tensors' device. The helpers of the timed path go through a small compiled module
 (``csrc/moe/helpers.cpp``), which does the same for calls that are right; the
 Python below it says what is wrong with the others and takes a caller's
 workspace. There is no CPU or PyTorch fallback.
@@ -17,6 +17,7 @@ workspace. There is no CPU or PyTorch fallback.
     q, scale = quantize_int8(w)                    # build time
     y = linear_int8(x, q, scale, bias)             # x quantized per token in the call
 """
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -151,6 +152,7 @@ def fp8w_moe_last_hip_error() -> int:
 # The handle of a device's current stream, without the stream object that torch.cuda.current_stream makes.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _STATUS = ("success", "invalid value (size, dtype, NULL pointer or overlapping buffers)", "misaligned pointer",
            "non-finite weight (NaN or infinity)", "workspace missing or too small", "HIP runtime error")
@@ -215,6 +217,15 @@ def _stream(device: torch.device) -> int:
     return _raw_stream(device.index)
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """The tensors' device made the current one for a call of the library: it launches on the current device, and
+    torch's default stream has the same handle (0) on each."""
+    return _SAME_DEVICE if device.index == _current_device() else torch.cuda.device(device)
+
+
 class Route(NamedTuple):
     weights: torch.Tensor  # [t, top_k] fp32
     experts: torch.Tensor  # [t, top_k] int32, -1: none
@@ -254,7 +265,8 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Route
            _want(out.slots, "slots", (t * top_k,), torch.int32, dev),
            _want(out.tokens, "tokens", (t * top_k,), torch.int32, dev)]
     workspace, wp, wb = _workspace(workspace, fp8w_route_workspace_bytes(t, e, top_k), dev)
-    st = fp8w_route(lp, _DT[logits.dtype], t, e, top_k, int(renormalize), *ptr, wp, wb, _stream(dev))
+    with _on(dev):
+        st = fp8w_route(lp, _DT[logits.dtype], t, e, top_k, int(renormalize), *ptr, wp, wb, _stream(dev))
     _check(st, "fp8w_route")
     return out
 
@@ -266,7 +278,8 @@ def quantize_experts(w: torch.Tensor):
     if w.dim() != 3:
         raise ValueError("w must be [e, n, k]")
     e, n, k = w.shape
-    q, scale = quantize(w.reshape(e * n, k))
+    with _on(w.device) if w.is_cuda else _SAME_DEVICE:
+        q, scale = quantize(w.reshape(e * n, k))
     return q.view(e, n, k), scale.view(e, n)
 
 
@@ -308,7 +321,8 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     yp = _want(out, "out", (m, n), x.dtype, dev)
     need = fp8w_linear_experts_workspace_bytes(m, e, n, k, xp, qp)
     workspace, wp, wb = _workspace(workspace, need, dev)
-    st = fp8w_linear_experts(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, wp, wb, _stream(dev))
+    with _on(dev):
+        st = fp8w_linear_experts(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, wp, wb, _stream(dev))
     _check(st, "fp8w_linear_experts")
     return out
 
@@ -329,7 +343,9 @@ def combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor = None) ->
     wp = _want(weights, "weights", (t, top), torch.float32, dev)
     if out is None:
         out = y.new_empty((t, n))
-    st = fp8w_combine(yp, act, wp, t, top, n, _want(out, "out", (t, n), y.dtype, dev), _stream(dev))
+    op = _want(out, "out", (t, n), y.dtype, dev)
+    with _on(dev):
+        st = fp8w_combine(yp, act, wp, t, top, n, op, _stream(dev))
     _check(st, "fp8w_combine")
     return out
 
@@ -344,8 +360,10 @@ def quantize_int8(w: torch.Tensor):
         raise TypeError(f"unsupported dtype {w.dtype}")
     q = torch.empty((n, k), dtype=torch.int8, device=dev)
     scale = torch.empty((n,), dtype=torch.float32, device=dev)
-    st = fp8w_quantize_int8(_want(w, "w", (n, k), w.dtype, dev), _DT[w.dtype], n, k, q.data_ptr() if q.numel() else 0,
-                            scale.data_ptr() if n else 0, _stream(dev))
+    wp = _want(w, "w", (n, k), w.dtype, dev)
+    with _on(dev):
+        st = fp8w_quantize_int8(wp, _DT[w.dtype], n, k, q.data_ptr() if q.numel() else 0, scale.data_ptr() if n else 0,
+                                _stream(dev))
     _check(st, "fp8w_quantize_int8")
     return q, scale
 
@@ -357,8 +375,10 @@ def quantize_activations_int8(x: torch.Tensor):
     m, k = x.shape
     qx = torch.empty((m, k), dtype=torch.int8, device=dev)
     sx = torch.empty((m,), dtype=torch.float32, device=dev)
-    st = fp8w_quantize_activations_int8(_want(x, "x", (m, k), x.dtype, dev), _act_code(x.dtype, "x"), m, k,
-                                        qx.data_ptr() if qx.numel() else 0, sx.data_ptr() if m else 0, _stream(dev))
+    xp, act = _want(x, "x", (m, k), x.dtype, dev), _act_code(x.dtype, "x")
+    with _on(dev):
+        st = fp8w_quantize_activations_int8(xp, act, m, k, qx.data_ptr() if qx.numel() else 0,
+                                            sx.data_ptr() if m else 0, _stream(dev))
     _check(st, "fp8w_quantize_activations_int8")
     return qx, sx
 
@@ -372,10 +392,11 @@ def gemm_int8(qx: torch.Tensor, sx: torch.Tensor, q: torch.Tensor, scale: torch.
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
     act = _act_code(out.dtype, "out")
-    st = fp8w_gemm_int8(_want(qx, "qx", (m, k), torch.int8, dev), _want(sx, "sx", (m,), torch.float32, dev), m, k,
-                        _want(q, "q", (n, k), torch.int8, dev), _want(scale, "scale", (n,), torch.float32, dev),
-                        _want(bias, "bias", (n,), out.dtype, dev), n, _want(out, "out", (m, n), out.dtype, dev), act,
-                        _stream(dev))
+    xp, tp = _want(qx, "qx", (m, k), torch.int8, dev), _want(sx, "sx", (m,), torch.float32, dev)
+    qp, sp = _want(q, "q", (n, k), torch.int8, dev), _want(scale, "scale", (n,), torch.float32, dev)
+    bp, yp = _want(bias, "bias", (n,), out.dtype, dev), _want(out, "out", (m, n), out.dtype, dev)
+    with _on(dev):
+        st = fp8w_gemm_int8(xp, tp, m, k, qp, sp, bp, n, yp, act, _stream(dev))
     _check(st, "fp8w_gemm_int8")
     return out
 
@@ -405,6 +426,7 @@ def linear_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
         out = x.new_empty((m, n))
     yp = _want(out, "out", (m, n), x.dtype, dev)
     workspace, wp, wb = _workspace(workspace, fp8w_linear_int8_workspace_bytes(m, n, k, xp, qp), dev)
-    st = fp8w_linear_int8(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, _stream(dev))
+    with _on(dev):
+        st = fp8w_linear_int8(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, _stream(dev))
     _check(st, "fp8w_linear_int8")
     return out

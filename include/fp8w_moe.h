@@ -5,7 +5,8 @@
  * C ABI of libfp8w_moe.so. The conventions are those of fp8w.h: dense row-major
  * tensors, device pointers owned by the caller, no allocation by the library,
  * work enqueued on `stream` (0 = the null stream) in stream order, arguments
- * validated before anything is enqueued, status codes and dtypes of fp8w.h.
+ * validated before anything is enqueued, status codes and dtypes of fp8w.h. The
+thread's current device is the buffers' and the stream's.
  * Every call is asynchronous and can be captured into a HIP graph, but for
  * fp8w_quantize_int8, which synchronizes. A call's results depend on its
  * arguments alone (no order of atomics enters them). Inputs may be read by whole
