@@ -224,10 +224,11 @@ fp8w_status_t fp8w_quantize_int8(const void* w, fp8w_dtype_t w_dtype, int64_t n,
     fp8w_status_t st = hip_status(fp8w::launch_quantize_int8(w, act_of(w_dtype), n, k, q, k, scale, stream));
     if (st != FP8W_SUCCESS)
         return st;
-    st = hip_status(hipMemcpyAsync(host.data(), scale, (size_t)n * 4, hipMemcpyDeviceToHost, stream));
+    st = hip_status(
+        fp8w::own_status(hipMemcpyAsync(host.data(), scale, (size_t)n * 4, hipMemcpyDeviceToHost, stream)));
     if (st != FP8W_SUCCESS)
         return st;
-    st = hip_status(hipStreamSynchronize(stream));
+    st = hip_status(fp8w::own_status(hipStreamSynchronize(stream)));
     if (st != FP8W_SUCCESS)
         return st;
     for (float s : host)

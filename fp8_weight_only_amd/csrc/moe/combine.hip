@@ -103,19 +103,15 @@ hipError_t launch_combine(const void* y, Act act, const float* weights, int64_t 
     const bool shift = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(2 * n)) & 3) != 0;
     const dim3 grid((unsigned)groups), block(kThreads);
 #define FP8W_COMBINE(A, TOP)                                                                                           \
-    if (shift)                                                                                                         \
-        hipLaunchKernelGGL((combine_kernel<A, TOP, true>), grid, block, 0, stream, src, weights, dst, items, (int)top, \
-                           n, chunks);                                                                                 \
-    else                                                                                                               \
-        hipLaunchKernelGGL((combine_kernel<A, TOP, false>), grid, block, 0, stream, src, weights, dst, items,          \
-                           (int)top, n, chunks)
+    return launch(shift ? combine_kernel<A, TOP, true> : combine_kernel<A, TOP, false>, grid, block, stream, src,      \
+                  weights, dst, items, top, n, chunks)
 #define FP8W_COMBINE_TOP(A)                                                                                            \
     switch (top) {                                                                                                     \
-    case 1: FP8W_COMBINE(A, 1); break;                                                                                 \
-    case 2: FP8W_COMBINE(A, 2); break;                                                                                 \
-    case 4: FP8W_COMBINE(A, 4); break;                                                                                 \
-    case 6: FP8W_COMBINE(A, 6); break;                                                                                 \
-    case 8: FP8W_COMBINE(A, 8); break;                                                                                 \
+    case 1: FP8W_COMBINE(A, 1);                                                                                        \
+    case 2: FP8W_COMBINE(A, 2);                                                                                        \
+    case 4: FP8W_COMBINE(A, 4);                                                                                        \
+    case 6: FP8W_COMBINE(A, 6);                                                                                        \
+    case 8: FP8W_COMBINE(A, 8);                                                                                        \
     default: FP8W_COMBINE(A, 0);                                                                                       \
     }
     if (act == Act::BF16) {
@@ -125,7 +121,6 @@ hipError_t launch_combine(const void* y, Act act, const float* weights, int64_t 
     }
 #undef FP8W_COMBINE_TOP
 #undef FP8W_COMBINE
-    return hipGetLastError();
 }
 
 }  // namespace fp8w

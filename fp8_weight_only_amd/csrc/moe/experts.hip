@@ -630,35 +630,25 @@ template <typename A, int CT, int W>
 hipError_t run_stream(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + 16 * CT - 1) / (16 * CT), groups = TN * max_row_tiles(c.m, c.e, 16);
-    if (shifted(c))
-        hipLaunchKernelGGL((experts_stream_kernel<A, CT, W, true>), dim3((unsigned)groups), dim3(W * kWave), 0,
-                           stream, c, (int)TN);
-    else
-        hipLaunchKernelGGL((experts_stream_kernel<A, CT, W, false>), dim3((unsigned)groups), dim3(W * kWave), 0,
-                           stream, c, (int)TN);
-    return hipGetLastError();
+    return launch(shifted(c) ? experts_stream_kernel<A, CT, W, true> : experts_stream_kernel<A, CT, W, false>,
+                  dim3((unsigned)groups), dim3(W * kWave), stream, c, TN);
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
 hipError_t run_tile(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + BN - 1) / BN, groups = TN * max_row_tiles(c.m, c.e, BM);
-    if (shifted(c))
-        hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM, true>), dim3((unsigned)groups),
-                           dim3(WN * WM * kWave), 0, stream, c, (int)TN);
-    else
-        hipLaunchKernelGGL((experts_tile_kernel<A, BN, BM, WN, WM, false>), dim3((unsigned)groups),
-                           dim3(WN * WM * kWave), 0, stream, c, (int)TN);
-    return hipGetLastError();
+    return launch(shifted(c) ? experts_tile_kernel<A, BN, BM, WN, WM, true>
+                             : experts_tile_kernel<A, BN, BM, WN, WM, false>,
+                  dim3((unsigned)groups), dim3(WN * WM * kWave), stream, c, TN);
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
 hipError_t run_ring(const ExpertCall& c, hipStream_t stream)
 {
     const int64_t TN = (c.n + BN - 1) / BN, groups = TN * max_row_tiles(c.m, c.e, BM);
-    hipLaunchKernelGGL((experts_ring_kernel<A, BN, BM, WN, WM, ring_depth(BN, BM)>), dim3((unsigned)groups),
-                       dim3(WN * WM * kWave), 0, stream, c, (int)TN);
-    return hipGetLastError();
+    return launch(experts_ring_kernel<A, BN, BM, WN, WM, ring_depth(BN, BM)>, dim3((unsigned)groups),
+                  dim3(WN * WM * kWave), stream, c, TN);
 }
 
 template <typename A>

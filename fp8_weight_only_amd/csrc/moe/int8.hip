@@ -864,26 +864,19 @@ template <typename A, int RT, int CT, int W, int U, bool FUSED>
 hipError_t run_stream(const Int8Call& c, const Int8Plan& p, hipStream_t stream)
 {
     const dim3 grid((unsigned)(p.TN * p.TM)), block(W * kWave);
-    if (shifted(c))
-        hipLaunchKernelGGL((int8_stream_kernel<A, RT, CT, W, U, FUSED, true>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM);
-    else
-        hipLaunchKernelGGL((int8_stream_kernel<A, RT, CT, W, U, FUSED, false>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM);
-    return hipGetLastError();
+    return launch(shifted(c) ? int8_stream_kernel<A, RT, CT, W, U, FUSED, true>
+                             : int8_stream_kernel<A, RT, CT, W, U, FUSED, false>,
+                  grid, block, stream, c, p.TN, p.TM);
 }
 
-// Joins the slices of a k split.
+// Joins the slices of a k split, behind a products' launch of this status.
 template <typename A>
-hipError_t join(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t stream)
+hipError_t join(hipError_t products, const Int8Call& c, const Int8Plan& p, int* part, hipStream_t stream)
 {
-    const hipError_t st = hipGetLastError();
-    if (st != hipSuccess || p.slices == 1)
-        return st;
+    if (products != hipSuccess || p.slices == 1)
+        return products;
     const int64_t items = c.m * ((c.n + 3) / 4);
-    hipLaunchKernelGGL(int8_join_kernel<A>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, stream, c, part,
-                       p.slices);
-    return hipGetLastError();
+    return launch(int8_join_kernel<A>, dim3((unsigned)((items + 255) / 256)), dim3(256), stream, c, part, p.slices);
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
@@ -892,22 +885,19 @@ hipError_t run_tile(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t
     const dim3 grid((unsigned)(p.TN * p.TM * p.slices)), block(WN * WM * kWave);
     const int stages = (int)(((c.k + 63) / 64 + p.slices - 1) / p.slices);
     int* sums = p.slices > 1 ? part : nullptr;
-    if (shifted(c))
-        hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, true>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM, stages, sums);
-    else
-        hipLaunchKernelGGL((int8_tile_kernel<A, BN, BM, WN, WM, false>), grid, block, 0, stream, c, (int)p.TN,
-                           (int)p.TM, stages, sums);
-    return join<A>(c, p, part, stream);
+    const hipError_t st = launch(shifted(c) ? int8_tile_kernel<A, BN, BM, WN, WM, true>
+                                            : int8_tile_kernel<A, BN, BM, WN, WM, false>,
+                                 grid, block, stream, c, p.TN, p.TM, stages, sums);
+    return join<A>(st, c, p, part, stream);
 }
 
 template <typename A, int BN, int BM, int WN, int WM, int NS>
 hipError_t run_ring(const Int8Call& c, const Int8Plan& p, int* part, hipStream_t stream)
 {
-    hipLaunchKernelGGL((int8_ring_kernel<A, BN, BM, WN, WM, NS>), dim3((unsigned)(p.TN * p.TM * p.slices)),
-                       dim3(WN * WM * kWave), 0, stream, c, (int)p.TN, (int)p.TM, (int)(c.k / 64 / p.slices),
-                       p.slices > 1 ? part : nullptr);
-    return join<A>(c, p, part, stream);
+    const hipError_t st =
+        launch(int8_ring_kernel<A, BN, BM, WN, WM, NS>, dim3((unsigned)(p.TN * p.TM * p.slices)),
+               dim3(WN * WM * kWave), stream, c, p.TN, p.TM, c.k / 64 / p.slices, p.slices > 1 ? part : nullptr);
+    return join<A>(st, c, p, part, stream);
 }
 
 template <typename A>
@@ -966,31 +956,25 @@ Int8Plan layer_plan(int64_t m, int64_t n, int64_t k, const int8_t* qw)
 // several times (fewer waves to join), 1024 below (22 rows of 14336: 4.3 us with
 // 256 threads).
 template <typename A>
-void run_quantize(const void* x, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale, hipStream_t stream)
+hipError_t run_quantize(const void* x, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale, hipStream_t stream)
 {
     const uint16_t* src = static_cast<const uint16_t*>(x);
     const bool shift = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(2 * k)) & 3) != 0;
     const bool few = rows < 1024;
 #define FP8W_ROW(NT, CH)                                                                                               \
-    if (shift)                                                                                                         \
-        hipLaunchKernelGGL((quantize_row_kernel<A, NT, CH, true>), dim3((unsigned)rows), dim3(NT), 0, stream, src, k,  \
-                           q, kx, scale);                                                                              \
-    else                                                                                                               \
-        hipLaunchKernelGGL((quantize_row_kernel<A, NT, CH, false>), dim3((unsigned)rows), dim3(NT), 0, stream, src, k, \
-                           q, kx, scale)
-    if (kx <= 2048) {
+    return launch(shift ? quantize_row_kernel<A, NT, CH, true> : quantize_row_kernel<A, NT, CH, false>,                \
+                  dim3((unsigned)rows), dim3(NT), stream, src, k, q, kx, scale)
+    if (kx <= 2048)
         FP8W_ROW(256, 1);
-    } else if (few && kx <= 8192) {
+    if (few && kx <= 8192)
         FP8W_ROW(1024, 1);
-    } else if (few) {
+    if (few)
         FP8W_ROW(1024, 2);
-    } else if (kx <= 4096) {
+    if (kx <= 4096)
         FP8W_ROW(256, 2);
-    } else if (kx <= 8192) {
+    if (kx <= 8192)
         FP8W_ROW(256, 4);
-    } else {
-        FP8W_ROW(256, 8);
-    }
+    FP8W_ROW(256, 8);
 #undef FP8W_ROW
 }
 
@@ -1004,12 +988,9 @@ hipError_t launch_quantize_int8(const void* x, Act type, int64_t rows, int64_t k
     if (!grid_fits(rows, 256))
         return hipErrorInvalidValue;
     if (type == Act::FP32 || kx > 16384)
-        hipLaunchKernelGGL(quantize_int8_kernel, dim3((unsigned)rows), dim3(256), 0, stream, x, type, k, q, kx, scale);
-    else if (type == Act::BF16)
-        run_quantize<Bf16>(x, rows, k, q, kx, scale, stream);
-    else
-        run_quantize<F16>(x, rows, k, q, kx, scale, stream);
-    return hipGetLastError();
+        return launch(quantize_int8_kernel, dim3((unsigned)rows), dim3(256), stream, x, type, k, q, kx, scale);
+    return type == Act::BF16 ? run_quantize<Bf16>(x, rows, k, q, kx, scale, stream)
+                             : run_quantize<F16>(x, rows, k, q, kx, scale, stream);
 }
 
 hipError_t launch_gemm_int8(const int8_t* qx, const float* sx, int64_t m, int64_t k, const int8_t* qw,

@@ -9,6 +9,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <tuple>
+
 namespace fp8w {
 
 enum class Act { BF16 = 0, FP16 = 1, FP32 = 2 };
@@ -16,6 +18,31 @@ enum class Act { BF16 = 0, FP16 = 1, FP32 = 2 };
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTop = 64;
 constexpr int64_t kMaxInt8K = 131072;  // 128 * 128 * k is at most 2^31
+
+// A HIP call's status. What a failed one leaves for hipGetLastError() is taken
+// back, for the status goes to the caller by itself.
+inline hipError_t own_status(hipError_t e)
+{
+    if (e != hipSuccess)
+        (void)hipGetLastError();
+    return e;
+}
+
+// Launches a kernel and returns the launch's own status. hipGetLastError() behind
+// it would return, and clear, an error that an earlier call of the thread left for
+// its own caller.
+template <typename... P, typename... Q>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t stream, Q... args)
+{
+    std::tuple<P...> values{static_cast<P>(args)...};
+    return std::apply(
+        [&](P&... v) {
+            void* pointers[] = {const_cast<void*>(static_cast<const void*>(&v))...};
+            return own_status(
+                hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, pointers, 0, stream));
+        },
+        values);
+}
 
 // A grid of this many workgroups of `threads` stays under the 2^32 threads a
 // launch can have.

@@ -556,23 +556,19 @@ template <int G, int J>
 hipError_t run(const void* logits, Act type, int64_t t, int e, int top, bool renorm, float* weights, int32_t* experts,
                int32_t* offsets, int32_t* slots, int32_t* tokens, void* ws, hipStream_t stream)
 {
-    if (small(t, e, top)) {
-        hipLaunchKernelGGL((route_small_kernel<G, J>), dim3(1), dim3(kThreads), 0, stream, logits, type, t, e, top,
-                           (int)renorm, weights, experts, offsets, slots, tokens);
-        return hipGetLastError();
-    }
+    if (small(t, e, top))
+        return launch(route_small_kernel<G, J>, dim3(1), dim3(kThreads), stream, logits, type, t, e, top, renorm,
+                      weights, experts, offsets, slots, tokens);
     const int64_t per = tokens_per_chunk(t);
     const int pitch = count_pitch(e);
     int32_t* counts = static_cast<int32_t*>(ws);
     const dim3 grid((unsigned)chunk_count(t)), block(kThreads);
-    hipLaunchKernelGGL((route_choose_kernel<G, J>), grid, block, 0, stream, logits, type, t, e, top, (int)renorm, per,
-                       weights, experts, counts, pitch);
-    const hipError_t st = hipGetLastError();
+    const hipError_t st = launch(route_choose_kernel<G, J>, grid, block, stream, logits, type, t, e, top, renorm, per,
+                                 weights, experts, counts, pitch);
     if (st != hipSuccess)
         return st;
-    hipLaunchKernelGGL(route_place_kernel, grid, block, 0, stream, experts, counts, pitch, t, e, top, per, offsets,
-                       slots, tokens);
-    return hipGetLastError();
+    return launch(route_place_kernel, grid, block, stream, experts, counts, pitch, t, e, top, per, offsets, slots,
+                  tokens);
 }
 
 }  // namespace

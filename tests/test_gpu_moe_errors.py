@@ -1,0 +1,87 @@
+"""What the mixture-of-experts and int8 calls make of HIP errors: those that an
+earlier call of the thread left for its own caller."""
+import ctypes
+
+import pytest
+import torch
+
+import fp8_weight_only_amd as fw
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+NO_DEVICE = 1 << 20
+
+
+@pytest.fixture
+def hip():
+    torch.cuda.init()
+    lib = ctypes.CDLL("libamdhip64.so.7")  # the one in the process
+    for name in ("hipStreamSynchronize", "hipStreamBeginCapture", "hipStreamEndCapture"):
+        getattr(lib, name).argtypes = {"hipStreamSynchronize": [ctypes.c_void_p],
+                                       "hipStreamBeginCapture": [ctypes.c_void_p, ctypes.c_int],
+                                       "hipStreamEndCapture": [ctypes.c_void_p, ctypes.c_void_p]}[name]
+    yield lib
+    lib.hipGetLastError()
+
+
+def _calls():
+    """name -> (a call through the C entry, its outputs), everything allocated."""
+    def zeros(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    g = torch.Generator(device="cuda").manual_seed(0)
+    t, e, top, n, k = 3000, 16, 2, 96, 256
+    logits = torch.randn((t, e), generator=g, device="cuda")
+    w, ex, off, sl, tok = zeros(t, top, dtype=torch.float32), zeros(t, top), zeros(e + 1), zeros(t * top), zeros(t * top)
+    need = fw.fp8w_route_workspace_bytes(t, e, top)
+    assert need > 0  # two launches
+    ws = zeros(need // 4)
+    y = torch.randn((64 * top, n), generator=g, device="cuda").to(BF)
+    cw, co = torch.rand((64, top), generator=g, device="cuda"), zeros(64, n, dtype=BF)
+    x = torch.randn((64, k), generator=g, device="cuda").to(BF)
+    q8 = torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    s8, qx, sx = torch.rand((n,), generator=g, device="cuda"), zeros(64, k, dtype=torch.int8), zeros(64, dtype=torch.float32)
+    y8, z8 = zeros(64, n, dtype=BF), zeros(64, n, dtype=BF)
+    ws8 = zeros(fw.fp8w_linear_int8_workspace_bytes(64, n, k, x.data_ptr(), q8.data_ptr()), dtype=torch.uint8)
+    qe = torch.randint(0, 120, (4, n, k), generator=g, device="cuda", dtype=torch.uint8)
+    se, oe = torch.rand((4, n), generator=g, device="cuda"), torch.tensor([0, 9, 20, 20, 64], device="cuda").int()
+    ye = zeros(64, n, dtype=BF)
+    stream = torch.cuda.current_stream().cuda_stream
+    p = torch.Tensor.data_ptr
+    keep = [logits, ws, y, cw, x, q8, s8, ws8, qe, se, oe]
+    return keep, {
+        "route": (lambda: fw.fp8w_route(p(logits), fw.FP32, t, e, top, 1, p(w), p(ex), p(off), p(sl), p(tok), p(ws), need,
+                                        stream), [w, ex, off, sl, tok]),
+        "combine": (lambda: fw.fp8w_combine(p(y), fw.BF16, p(cw), 64, top, n, p(co), stream), [co]),
+        "experts": (lambda: fw.fp8w_linear_experts(p(x), fw.BF16, 64, k, p(qe), p(se), 0, 4, n, p(oe), 64, 0, 0, p(ye), 0,
+                                                   0, stream), [ye]),
+        "quantize": (lambda: fw.fp8w_quantize_activations_int8(p(x), fw.BF16, 64, k, p(qx), p(sx), stream), [qx, sx]),
+        "gemm": (lambda: fw.fp8w_gemm_int8(p(qx), p(sx), 64, k, p(q8), p(s8), 0, n, p(z8), fw.BF16, stream), [z8]),
+        "linear": (lambda: fw.fp8w_linear_int8(p(x), fw.BF16, 64, k, p(q8), p(s8), 0, n, p(y8), p(ws8), ws8.numel(),
+                                               stream), [y8]),
+        "weights": (lambda: fw.fp8w_quantize_int8(p(x), fw.BF16, 64, k, p(qx), p(sx), stream), [qx, sx]),
+    }
+
+
+def test_an_error_left_by_an_earlier_call_is_not_the_launch_s(hip):
+    """A call neither fails for it nor takes it from its owner."""
+    keep, calls = _calls()
+    want = {}
+    for name, (call, outs) in calls.items():
+        assert call() == fw.SUCCESS
+        torch.cuda.synchronize()
+        want[name] = [o.clone() for o in outs]
+    for name, (call, outs) in calls.items():
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    for name, (call, outs) in calls.items():
+        hip.hipGetLastError()
+        left = hip.hipSetDevice(NO_DEVICE)
+        assert left != 0 and hip.hipPeekAtLastError() == left
+        status = call()
+        after = hip.hipGetLastError()
+        torch.cuda.synchronize()
+        assert status == fw.SUCCESS, name
+        assert after == left, f"{name}: the error was taken from its owner"
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[name])), name
