@@ -4,9 +4,10 @@
 // 13 us and a weighted sum 8, of which the kernels take 5 and 2.
 //
 // Each function returns None for arguments that it does not take (a wrong type,
-// shape, device or layout) and for a call that the library refused; moe.py then
-// goes through the same call step by step and raises what is wrong. Nothing is
-// launched twice: the library refuses before it enqueues anything.
+// shape, device or layout) and for a call that the library refused, which it does
+// before it enqueues anything; moe.py then goes through the same call step by step
+// and raises what is wrong. A call that failed in HIP may have enqueued some of its
+// kernels: its status is returned, for moe.py to raise, and it is not tried again.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -104,6 +105,12 @@ fp8w_status_t without_gil(F&& f)
     return st;
 }
 
+// What a call that did not succeed returns.
+PyObject* failed(fp8w_status_t st)
+{
+    return st == FP8W_ERR_HIP ? PyLong_FromLong(st) : none();
+}
+
 // combine(y, weights, out)
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
@@ -124,7 +131,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n)
             return fp8w_combine(y.ptr(), act, static_cast<const float*>(w.ptr()), t, top, c,
                                 made.numel() ? made.data_ptr() : nullptr, stream);
         });
-        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : none();
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
     });
 }
 
@@ -159,7 +166,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
                               p + 2 * s, p + 3 * s, need ? p + 4 * s + e + 1 : nullptr, need, stream);
         });
         if (st != FP8W_SUCCESS)
-            return none();
+            return failed(st);
         auto list = [&](int64_t first, int64_t count) { return buf.as_strided({count}, {1}, first); };
         auto table = [&](const at::Tensor& b, int64_t first) { return b.as_strided({t, top}, {top, 1}, first); };
         PyObject* r = PyTuple_New(5);
@@ -206,7 +213,7 @@ PyObject* linear_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
                                        made.numel() ? made.data_ptr() : nullptr, need ? ws.data_ptr() : nullptr, need,
                                        stream);
         });
-        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : none();
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
     });
 }
 
@@ -237,7 +244,7 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
                                     made.numel() ? made.data_ptr() : nullptr, need ? ws.data_ptr() : nullptr, need,
                                     stream);
         });
-        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : none();
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
     });
 }
 

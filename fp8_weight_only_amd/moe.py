@@ -4,10 +4,11 @@ A thin ctypes binding over ``libfp8w_moe.so`` (declared in
 ``include/fp8w_moe.h``), in the manner of the package's FP8 linear layer: the
 raw entry points keep the C names and take integers; the tensor helpers check
 their arguments, allocate outputs and workspaces with torch and run on torch's
-current stream of the tensors' device. The helpers of the timed path go through a small compiled module
-(``csrc/moe/helpers.cpp``), which does the same for calls that are right; the
-Python below it says what is wrong with the others and takes a caller's
-workspace. There is no CPU or PyTorch fallback.
+current stream of the tensors' device. The helpers of the timed path go through
+a small compiled module (``csrc/moe/helpers.cpp``), which does the same for calls
+that are right (and returns the status of a launch that failed); the Python below
+it says what is wrong with the others and takes a caller's workspace. There is no
+CPU or PyTorch fallback.
 
     r = route(logits, top_k)                       # who goes where
     h = linear_experts(x, q, scale, r.offsets, x_rows=r.tokens)     # up: gathers tokens, rows by expert
@@ -246,7 +247,7 @@ def route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out: Route
     if out is None and workspace is None:
         r = (_FAST or _fast()).route(logits, top_k, renormalize)
         if r is not None:
-            return Route._make(r)
+            return Route._make(r) if type(r) is not int else _check(r, "fp8w_route")
     dev = _gpu(logits, "logits", 2)
     t, e = logits.shape
     if logits.dtype not in _DT:
@@ -301,7 +302,7 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     if workspace is None:
         r = (_FAST or _fast()).linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out)
         if r is not None:
-            return r
+            return r if type(r) is not int else _check(r, "fp8w_linear_experts")
     dev = _gpu(x, "x", 2)
     if q.dim() != 3:
         raise ValueError("q must have 3 dimensions")
@@ -332,7 +333,7 @@ def combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor = None) ->
     y [t * top_k, n] bf16 / fp16 (rows by slot), weights [t, top_k] fp32."""
     r = (_FAST or _fast()).combine(y, weights, out)
     if r is not None:
-        return r
+        return r if type(r) is not int else _check(r, "fp8w_combine")
     dev = _gpu(y, "y", 2)
     if weights.dim() != 2:
         raise ValueError("weights must have 2 dimensions")
@@ -413,7 +414,7 @@ def linear_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
     if workspace is None:
         r = (_FAST or _fast()).linear_int8(x, q, scale, bias, out)
         if r is not None:
-            return r
+            return r if type(r) is not int else _check(r, "fp8w_linear_int8")
     dev = _gpu(x, "x", 2)
     m, k = x.shape
     n = q.shape[0]

@@ -1,5 +1,5 @@
 """What the mixture-of-experts and int8 calls make of HIP errors: those that an
-earlier call of the thread left for its own caller."""
+earlier call of the thread left for its own caller, and launches that fail."""
 import ctypes
 
 import pytest
@@ -16,10 +16,9 @@ NO_DEVICE = 1 << 20
 def hip():
     torch.cuda.init()
     lib = ctypes.CDLL("libamdhip64.so.7")  # the one in the process
-    for name in ("hipStreamSynchronize", "hipStreamBeginCapture", "hipStreamEndCapture"):
-        getattr(lib, name).argtypes = {"hipStreamSynchronize": [ctypes.c_void_p],
-                                       "hipStreamBeginCapture": [ctypes.c_void_p, ctypes.c_int],
-                                       "hipStreamEndCapture": [ctypes.c_void_p, ctypes.c_void_p]}[name]
+    lib.hipStreamCreate.argtypes = lib.hipStreamDestroy.argtypes = lib.hipStreamSynchronize.argtypes = [ctypes.c_void_p]
+    lib.hipStreamBeginCapture.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    lib.hipStreamEndCapture.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     yield lib
     lib.hipGetLastError()
 
@@ -85,3 +84,31 @@ def test_an_error_left_by_an_earlier_call_is_not_the_launch_s(hip):
         assert status == fw.SUCCESS, name
         assert after == left, f"{name}: the error was taken from its owner"
         assert all(torch.equal(a, b) for a, b in zip(outs, want[name])), name
+
+
+def test_a_failed_launch_is_raised_and_not_tried_again(hip, monkeypatch):
+    """A launch into a capture that has become invalid is refused by HIP."""
+    y, w = torch.ones((6, 40), dtype=BF, device="cuda"), torch.full((3, 2), 0.5, device="cuda")
+    out = torch.zeros((3, 40), dtype=BF, device="cuda")
+    again = []
+    entry = fw.moe.fp8w_combine
+    monkeypatch.setattr(fw.moe, "fp8w_combine", lambda *a: again.append(a) or entry(*a))
+    torch.cuda.synchronize()
+    own = ctypes.c_void_p()  # not one of torch's pool: it stays invalid
+    assert hip.hipStreamCreate(ctypes.byref(own)) == 0
+    try:
+        assert hip.hipStreamBeginCapture(own, 2) == 0
+        assert hip.hipStreamSynchronize(own) != 0  # not allowed while capturing: the capture is invalid
+        with torch.cuda.stream(torch.cuda.ExternalStream(own.value)):
+            with pytest.raises(fw.Fp8wMoeError) as err:
+                fw.combine(y, w, out)
+    finally:
+        graph = ctypes.c_void_p()
+        hip.hipStreamEndCapture(own, ctypes.byref(graph))
+        hip.hipStreamDestroy(own)
+        hip.hipGetLastError()
+    assert err.value.status == fw.ERR_HIP and fw.fp8w_moe_last_hip_error() != 0
+    assert not again, "enqueued once more"
+    fw.combine(y, w, out)
+    torch.cuda.synchronize()
+    assert (out == 1).all()
