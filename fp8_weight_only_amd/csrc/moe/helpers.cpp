@@ -13,7 +13,10 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
 
 #include "../../../include/fp8w_moe.h"
 
@@ -80,17 +83,15 @@ PyObject* none()
 // The launches and allocations of a call go to its first tensor's device.
 #define FP8W_ON_DEVICE_OF(arg) const c10::DeviceGuard on_device((arg).t->device())
 
-// Runs f, and turns a C++ exception into a Python one.
+// Runs f, and turns a C++ exception into the Python one that torch's own calls
+// raise for it (torch.OutOfMemoryError where an allocation failed).
 template <typename F>
 PyObject* guarded(F&& f)
 {
     try {
         return f();
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     } catch (...) {
-        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+        torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

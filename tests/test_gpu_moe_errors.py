@@ -1,5 +1,6 @@
 """What the mixture-of-experts and int8 calls make of HIP errors: those that an
-earlier call of the thread left for its own caller, and launches that fail."""
+earlier call of the thread left for its own caller, launches that fail, and
+allocations that do."""
 import ctypes
 
 import pytest
@@ -112,3 +113,15 @@ def test_a_failed_launch_is_raised_and_not_tried_again(hip, monkeypatch):
     fw.combine(y, w, out)
     torch.cuda.synchronize()
     assert (out == 1).all()
+
+
+def test_a_failed_allocation_raises_torch_s_error():
+    """An output larger than the GPU's memory, through the compiled helpers as through Python."""
+    m, n, k = 1 << 21, 1 << 18, 16
+    x = torch.zeros((m, k), dtype=BF, device="cuda")
+    q, s = torch.zeros((n, k), dtype=torch.int8, device="cuda"), torch.zeros((n,), device="cuda")
+    for extra in ({}, {"workspace": torch.zeros(16, dtype=torch.uint8, device="cuda")}):
+        with pytest.raises(torch.OutOfMemoryError):
+            fw.linear_int8(x, q, s, **extra)
+    y = fw.linear_int8(x[:64], q[:64], s[:64])
+    assert (y == 0).all()
