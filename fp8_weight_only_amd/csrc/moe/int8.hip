@@ -983,14 +983,24 @@ hipError_t run_quantize(const void* x, int64_t rows, int64_t k, int8_t* q, int64
 hipError_t launch_quantize_int8(const void* x, Act type, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale,
                                 hipStream_t stream)
 {
-    if (rows == 0)
-        return hipSuccess;
-    if (!grid_fits(rows, 256))
-        return hipErrorInvalidValue;
-    if (type == Act::FP32 || kx > 16384)
-        return launch(quantize_int8_kernel, dim3((unsigned)rows), dim3(256), stream, x, type, k, q, kx, scale);
-    return type == Act::BF16 ? run_quantize<Bf16>(x, rows, k, q, kx, scale, stream)
-                             : run_quantize<F16>(x, rows, k, q, kx, scale, stream);
+    // a workgroup per row: 2^23 rows of 256 threads are half of what a launch can have
+    constexpr int64_t kRows = (int64_t)1 << 23;
+    const uint8_t* src = static_cast<const uint8_t*>(x);
+    for (int64_t r = 0; r < rows; r += kRows) {
+        const int64_t part = rows - r < kRows ? rows - r : kRows;
+        const void* from = src + r * k * (type == Act::FP32 ? 4 : 2);
+        int8_t* codes = q + r * kx;
+        hipError_t st;
+        if (type == Act::FP32 || kx > 16384)
+            st = launch(quantize_int8_kernel, dim3((unsigned)part), dim3(256), stream, from, type, k, codes, kx,
+                        scale + r);
+        else
+            st = type == Act::BF16 ? run_quantize<Bf16>(from, part, k, codes, kx, scale + r, stream)
+                                   : run_quantize<F16>(from, part, k, codes, kx, scale + r, stream);
+        if (st != hipSuccess)
+            return st;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_gemm_int8(const int8_t* qx, const float* sx, int64_t m, int64_t k, const int8_t* qw,

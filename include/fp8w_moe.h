@@ -11,8 +11,8 @@ thread's current device is the buffers' and the stream's.
  * fp8w_quantize_int8, which synchronizes. A call's results depend on its
  * arguments alone (no order of atomics enters them). Inputs may be read by whole
  * aligned dwords, that is with up to three bytes beside their first and last. Sizes up to 2^31 - 1
- * unless stated; a call that would need a launch of 2^32 threads or more (some
- * 6e10 outputs) is invalid.
+ * unless stated; a call whose products or sums would need a launch of 2^32 threads
+ * or more (above 3e10 outputs) is invalid.
  */
 #ifndef FP8W_MOE_H
 #define FP8W_MOE_H
