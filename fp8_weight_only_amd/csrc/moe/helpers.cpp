@@ -182,7 +182,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out), the workspace its own
+// linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out)
 PyObject* linear_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -199,20 +199,15 @@ PyObject* linear_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
             !b.like(x, x.type(), {e, c}) || !xr.like(x, at::kInt, {m}) || !yr.like(x, at::kInt, {m}) ||
             !out.like(x, x.type(), {m, c}))
             return none();
-        const uint8_t* qp = static_cast<const uint8_t*>(q.ptr());
-        const size_t need = fp8w_linear_experts_workspace_bytes(m, e, c, k, x.ptr(), qp);
         FP8W_ON_DEVICE_OF(x);
         const at::Tensor made = out.given ? *out.t : make(x, {m, c}, x.type());
-        at::Tensor ws;
-        if (need)
-            ws = make(x, {(int64_t)need}, at::kByte);
         const hipStream_t stream = stream_of(x);
         const fp8w_status_t st = without_gil([&] {
-            return fp8w_linear_experts(x.ptr(), act, rows, k, qp, static_cast<const float*>(s.ptr()), b.ptr(), e, c,
+            return fp8w_linear_experts(x.ptr(), act, rows, k, static_cast<const uint8_t*>(q.ptr()),
+                                       static_cast<const float*>(s.ptr()), b.ptr(), e, c,
                                        static_cast<const int32_t*>(off.ptr()), m,
                                        static_cast<const int32_t*>(xr.ptr()), static_cast<const int32_t*>(yr.ptr()),
-                                       made.numel() ? made.data_ptr() : nullptr, need ? ws.data_ptr() : nullptr, need,
-                                       stream);
+                                       made.numel() ? made.data_ptr() : nullptr, nullptr, 0, stream);
         });
         return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
     });

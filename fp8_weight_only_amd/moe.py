@@ -298,11 +298,12 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     x: [rows, k] bf16 / fp16; q: [e, n, k] uint8 codes; scale: [e, n] fp32;
     bias: [e, n] of x.dtype; offsets: [e + 1] int32; x_rows / y_rows: [m] int32
     (without them position p reads row p / writes row p). Rows of positions from
-    offsets[e] on are zeros. With ``x_rows`` m is its length, else x's."""
-    if workspace is None:
-        r = (_FAST or _fast()).linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out)
-        if r is not None:
-            return r if type(r) is not int else _check(r, "fp8w_linear_experts")
+    offsets[e] on are zeros. With ``x_rows`` m is its length, else x's. No
+    workspace is needed (experts_workspace_bytes is 0); one that is given is not
+    used."""
+    r = (_FAST or _fast()).linear_experts(x, q, scale, offsets, bias, x_rows, y_rows, out)
+    if r is not None:
+        return r if type(r) is not int else _check(r, "fp8w_linear_experts")
     dev = _gpu(x, "x", 2)
     if q.dim() != 3:
         raise ValueError("q must have 3 dimensions")
@@ -320,10 +321,8 @@ def linear_experts(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offset
     if out is None:
         out = x.new_empty((m, n))
     yp = _want(out, "out", (m, n), x.dtype, dev)
-    need = fp8w_linear_experts_workspace_bytes(m, e, n, k, xp, qp)
-    workspace, wp, wb = _workspace(workspace, need, dev)
     with _on(dev):
-        st = fp8w_linear_experts(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, wp, wb, _stream(dev))
+        st = fp8w_linear_experts(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, 0, 0, _stream(dev))
     _check(st, "fp8w_linear_experts")
     return out
 

@@ -6,13 +6,13 @@
  * tensors, device pointers owned by the caller, no allocation by the library,
  * work enqueued on `stream` (0 = the null stream) in stream order, arguments
  * validated before anything is enqueued, status codes and dtypes of fp8w.h. The
-thread's current device is the buffers' and the stream's.
- * Every call is asynchronous and can be captured into a HIP graph, but for
- * fp8w_quantize_int8, which synchronizes. A call's results depend on its
- * arguments alone (no order of atomics enters them). Inputs may be read by whole
- * aligned dwords, that is with up to three bytes beside their first and last. Sizes up to 2^31 - 1
- * unless stated; a call whose products or sums would need a launch of 2^32 threads
- * or more (above 3e10 outputs) is invalid.
+ * thread's current device is the buffers' and the stream's. Every call is
+ * asynchronous and can be captured into a HIP graph, but for fp8w_quantize_int8,
+ * which synchronizes. A call's results depend on its arguments alone (no order of
+ * atomics enters them). Inputs may be read by whole aligned dwords, that is with
+ * up to three bytes beside their first and last. Sizes up to 2^31 - 1 unless
+ * stated; a call whose products or sums would need a launch of 2^32 threads or
+ * more (above 3e10 outputs) is invalid.
  */
 #ifndef FP8W_MOE_H
 #define FP8W_MOE_H
@@ -66,7 +66,7 @@ FP8W_API size_t fp8w_route_workspace_bytes(int64_t t, int64_t e, int64_t top_k);
  *   x_rows, y_rows  [m] int32 on the device, or NULL; dst(p) = y_rows[p], or p.
  *            y_rows must not name a row twice.
  *   y        [m, n] of act_dtype; must not overlap an input.
- *   workspace, workspace_bytes: not used by the present plans.
+ *   workspace, workspace_bytes: not used, whatever they are (no plan needs one).
  * Device values are not validated, and nothing outside the buffers is touched
  * whatever they hold: offsets are clamped to 0 .. m, a position whose src is
  * outside x gives a row of NaN, one whose dst is outside y is not written.
@@ -77,12 +77,13 @@ FP8W_API fp8w_status_t fp8w_linear_experts(const void* x, fp8w_dtype_t act_dtype
                                            const int32_t* y_rows, void* y, void* workspace, size_t workspace_bytes,
                                            hipStream_t stream);
 
-/* Workspace bytes fp8w_linear_experts uses: 0 in this version. */
+/* Workspace bytes fp8w_linear_experts uses: 0. */
 FP8W_API size_t fp8w_linear_experts_workspace_bytes(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                     const uint8_t* q);
 
-/* Name of the kernel fp8w_linear_experts runs for an x of up to m rows, NULL for invalid sizes and calls that run none. The string lives until the thread's
- * next call. */
+/* Name of the kernel fp8w_linear_experts runs for an x of up to m rows, NULL for
+ * invalid sizes and calls that run none. The string lives until the thread's next
+ * call. */
 FP8W_API const char* fp8w_linear_experts_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                 const uint8_t* q);
 
