@@ -3,11 +3,13 @@
 // fp32 products and sums in the order of j, one rounding to the activation type.
 //
 // A stream of top + 1 rows per token, bound by memory. Each thread owns eight
-// channels (16 bytes) of one token and loads them from every row before the first
-// product needs them (top 1, 2, 4, 6, 8 are known when compiled), past the
-// caches, since nothing is read twice: 8192 tokens, 8 rows of 4096 in 96 us,
-// 6.3 TB/s (a loop over the rows with cached loads: 113; a large copy: 5.2 TB/s).
-// Odd widths run the same code on rows at any byte: 8 rows of 4095 in 117 us.
+// channels (16 bytes) of one token. Where top is 1, 2, 4, 6 or 8 (known when
+// compiled) it loads them from every row before the first product needs them,
+// past the caches, since nothing is read twice: 8192 tokens, 8 rows of 4096 in
+// 96 us, 6.3 TB/s (a loop over the rows with cached loads: 113; a large copy: 5.2
+// TB/s); rows below dword alignment by whole dwords shifted (8 rows of 4095: 116
+// us). Any other top takes the loop: 8192 tokens, 3 rows of 4096 in 47 us, 5.7 TB/s,
+// and 3 rows of 4095 in 55, where 2 rows of 4096 by the loads ahead take 32, 6.4.
 #include "device.hpp"
 #include "moe.hpp"
 
@@ -16,7 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// TOP > 0: top, known when compiled; 0: any.
+// TOP > 0: top, known when compiled; 0: any (a loop, rows at any byte).
 template <typename A, int TOP, bool SHIFT>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const uint16_t* __restrict__ y,
                                                            const float* __restrict__ weights,
@@ -103,8 +105,8 @@ hipError_t launch_combine(const void* y, Act act, const float* weights, int64_t 
     const bool shift = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(2 * n)) & 3) != 0;
     const dim3 grid((unsigned)groups), block(kThreads);
 #define FP8W_COMBINE(A, TOP)                                                                                           \
-    return launch(shift ? combine_kernel<A, TOP, true> : combine_kernel<A, TOP, false>, grid, block, stream, src,      \
-                  weights, dst, items, top, n, chunks)
+    return launch(shift && TOP ? combine_kernel<A, TOP, (TOP > 0)> : combine_kernel<A, TOP, false>, grid, block,       \
+                  stream, src, weights, dst, items, top, n, chunks)
 #define FP8W_COMBINE_TOP(A)                                                                                            \
     switch (top) {                                                                                                     \
     case 1: FP8W_COMBINE(A, 1);                                                                                        \
