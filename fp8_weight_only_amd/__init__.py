@@ -29,6 +29,7 @@ import torch
 
 from . import moe
 from .moe import *  # noqa: F401,F403  (routing, products grouped by expert, the int8 layer)
+from .moe import _on
 
 __all__ = [
     *moe.__all__,
@@ -271,8 +272,9 @@ def quantize(w: torch.Tensor):
     n, k = w.shape
     q = torch.empty((n, k), dtype=torch.uint8, device=w.device)
     scale = torch.empty((n,), dtype=torch.float32, device=w.device)
-    st = fp8w_quantize(_dev(w, "w") if w.numel() else 0, _dtype_code(w.dtype), n, k,
-                       q.data_ptr() if q.numel() else 0, scale.data_ptr() if n else 0, _stream(w.device))
+    with _on(w.device):
+        st = fp8w_quantize(_dev(w, "w") if w.numel() else 0, _dtype_code(w.dtype), n, k,
+                           q.data_ptr() if q.numel() else 0, scale.data_ptr() if n else 0, _stream(w.device))
     _check(st, "fp8w_quantize")
     return q, scale
 
@@ -324,7 +326,8 @@ def linear(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: torch.Te
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     wp = _dev(workspace, "workspace") if workspace is not None and workspace.numel() else 0
     wb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = fp8w_linear_with_path(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, path, _stream(x.device))
+    with _on(x.device):
+        st = fp8w_linear_with_path(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, path, _stream(x.device))
     _check(st, "fp8w_linear")
     return out
 
@@ -346,10 +349,11 @@ def linear_noalloc(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: 
         out = torch.empty((m, n), dtype=x.dtype, device=x.device)
     elif out.shape != (m, n) or out.dtype != x.dtype:
         raise ValueError("out must be [m, n] in the activation dtype")
-    st = fp8w_linear_noalloc(_dev(x, "x") if x.numel() else 0, _dtype_code(x.dtype), m, k,
-                             _dev(q, "q") if q.numel() else 0, _dev(scale, "scale") if n else 0,
-                             _dev(bias, "bias") if bias is not None and n else 0, n,
-                             _dev(out, "out") if out.numel() else 0, _stream(x.device))
+    with _on(x.device):
+        st = fp8w_linear_noalloc(_dev(x, "x") if x.numel() else 0, _dtype_code(x.dtype), m, k,
+                                 _dev(q, "q") if q.numel() else 0, _dev(scale, "scale") if n else 0,
+                                 _dev(bias, "bias") if bias is not None and n else 0, n,
+                                 _dev(out, "out") if out.numel() else 0, _stream(x.device))
     _check(st, "fp8w_linear_noalloc")
     return out
 
@@ -359,10 +363,11 @@ def dequantize(q: torch.Tensor, scale: torch.Tensor = None, dtype: torch.dtype =
     or the exact unscaled values when scale is None."""
     n, k = q.shape
     out = torch.empty((n, k), dtype=dtype, device=q.device)
-    st = fp8w_dequantize_fallback(_dev(q, "q") if q.numel() else 0,
-                                  _dev(scale, "scale") if scale is not None and n else 0,
-                                  n, k, out.data_ptr() if out.numel() else 0, _dtype_code(dtype),
-                                  _stream(q.device))
+    with _on(q.device):
+        st = fp8w_dequantize_fallback(_dev(q, "q") if q.numel() else 0,
+                                      _dev(scale, "scale") if scale is not None and n else 0,
+                                      n, k, out.data_ptr() if out.numel() else 0, _dtype_code(dtype),
+                                      _stream(q.device))
     _check(st, "fp8w_dequantize_fallback")
     return out
 
@@ -378,9 +383,10 @@ def quantize_grouped(w: torch.Tensor, group: int):
         raise ValueError("group must divide k")
     q = torch.empty((n, k), dtype=torch.uint8, device=w.device)
     scale = torch.empty((n, k // group), dtype=torch.float32, device=w.device)
-    st = fp8w_quantize_grouped(_dev(w, "w") if w.numel() else 0, _dtype_code(w.dtype), n, k, group,
-                               q.data_ptr() if q.numel() else 0, scale.data_ptr() if scale.numel() else 0,
-                               _stream(w.device))
+    with _on(w.device):
+        st = fp8w_quantize_grouped(_dev(w, "w") if w.numel() else 0, _dtype_code(w.dtype), n, k, group,
+                                   q.data_ptr() if q.numel() else 0, scale.data_ptr() if scale.numel() else 0,
+                                   _stream(w.device))
     _check(st, "fp8w_quantize_grouped")
     return q, scale
 
@@ -422,10 +428,11 @@ def linear_grouped(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: 
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     wp = _dev(workspace, "workspace") if workspace is not None and workspace.numel() else 0
     wb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = fp8w_linear_grouped_with_workspace(xp, act, m, k, qp, _dev(scale, "scale"), group,
-                                            _dev(bias, "bias") if bias is not None and n else 0, n,
-                                            _dev(out, "out") if out.numel() else 0, wp, wb, path,
-                                            _stream(x.device))
+    with _on(x.device):
+        st = fp8w_linear_grouped_with_workspace(xp, act, m, k, qp, _dev(scale, "scale"), group,
+                                                _dev(bias, "bias") if bias is not None and n else 0, n,
+                                                _dev(out, "out") if out.numel() else 0, wp, wb, path,
+                                                _stream(x.device))
     _check(st, "fp8w_linear_grouped")
     return out
 
@@ -435,8 +442,9 @@ def dequantize_grouped(q: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype 
     n, k = q.shape
     group = k // scale.shape[1]
     out = torch.empty((n, k), dtype=dtype, device=q.device)
-    st = fp8w_dequantize_grouped(_dev(q, "q"), _dev(scale, "scale"), group, n, k, out.data_ptr(),
-                                 _dtype_code(dtype), _stream(q.device))
+    with _on(q.device):
+        st = fp8w_dequantize_grouped(_dev(q, "q"), _dev(scale, "scale"), group, n, k, out.data_ptr(),
+                                     _dtype_code(dtype), _stream(q.device))
     _check(st, "fp8w_dequantize_grouped")
     return out
 
@@ -447,8 +455,9 @@ def quantize_activations(x: torch.Tensor):
     m, k = x.shape
     qx = torch.empty((m, k), dtype=torch.uint8, device=x.device)
     sx = torch.empty((m,), dtype=torch.float32, device=x.device)
-    st = fp8w_quantize_activations(_dev(x, "x") if x.numel() else 0, _dtype_code(x.dtype), m, k,
-                                   qx.data_ptr() if qx.numel() else 0, sx.data_ptr() if m else 0, _stream(x.device))
+    with _on(x.device):
+        st = fp8w_quantize_activations(_dev(x, "x") if x.numel() else 0, _dtype_code(x.dtype), m, k,
+                                       qx.data_ptr() if qx.numel() else 0, sx.data_ptr() if m else 0, _stream(x.device))
     _check(st, "fp8w_quantize_activations")
     return qx, sx
 
@@ -460,9 +469,10 @@ def gemm_w8a8(qx: torch.Tensor, sx: torch.Tensor, q: torch.Tensor, scale: torch.
     n = q.shape[0]
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=qx.device)
-    st = fp8w_gemm_w8a8(_dev(qx, "qx"), _dev(sx, "sx"), m, k, _dev(q, "q"), _dev(scale, "scale"),
-                        _dev(bias, "bias") if bias is not None else 0, n, _dev(out, "out"),
-                        _dtype_code(out.dtype), _stream(qx.device))
+    with _on(qx.device):
+        st = fp8w_gemm_w8a8(_dev(qx, "qx"), _dev(sx, "sx"), m, k, _dev(q, "q"), _dev(scale, "scale"),
+                            _dev(bias, "bias") if bias is not None else 0, n, _dev(out, "out"),
+                            _dtype_code(out.dtype), _stream(qx.device))
     _check(st, "fp8w_gemm_w8a8")
     return out
 
@@ -478,10 +488,11 @@ def linear_w8a8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
         workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
     if out is None:
         out = torch.empty((m, n), dtype=x.dtype, device=x.device)
-    st = fp8w_linear_w8a8(_dev(x, "x"), _dtype_code(x.dtype), m, k, _dev(q, "q"), _dev(scale, "scale"),
-                          _dev(bias, "bias") if bias is not None else 0, n, _dev(out, "out"),
-                          _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-                          _stream(x.device))
+    with _on(x.device):
+        st = fp8w_linear_w8a8(_dev(x, "x"), _dtype_code(x.dtype), m, k, _dev(q, "q"), _dev(scale, "scale"),
+                              _dev(bias, "bias") if bias is not None else 0, n, _dev(out, "out"),
+                              _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                              _stream(x.device))
     _check(st, "fp8w_linear_w8a8")
     return out
 
@@ -493,7 +504,8 @@ def fnuz_to_ocp(codes: torch.Tensor, out: torch.Tensor = None) -> torch.Tensor:
     if out is None:
         out = torch.empty_like(src)
     n = src.numel()
-    st = fp8w_fnuz_to_ocp(_dev(src, "codes") if n else 0, n, _dev(out, "out") if n else 0, _stream(src.device))
+    with _on(src.device):
+        st = fp8w_fnuz_to_ocp(_dev(src, "codes") if n else 0, n, _dev(out, "out") if n else 0, _stream(src.device))
     _check(st, "fp8w_fnuz_to_ocp")
     return out
 

@@ -224,7 +224,9 @@ _SAME_DEVICE = contextlib.nullcontext()
 def _on(device: torch.device):
     """The tensors' device made the current one for a call of the library: it launches on the current device, and
     torch's default stream has the same handle (0) on each."""
-    return _SAME_DEVICE if device.index == _current_device() else torch.cuda.device(device)
+    if device.type != "cuda" or device.index == _current_device():  # others are refused by the argument checks
+        return _SAME_DEVICE
+    return torch.cuda.device(device)
 
 
 class Route(NamedTuple):
@@ -279,8 +281,7 @@ def quantize_experts(w: torch.Tensor):
     if w.dim() != 3:
         raise ValueError("w must be [e, n, k]")
     e, n, k = w.shape
-    with _on(w.device) if w.is_cuda else _SAME_DEVICE:
-        q, scale = quantize(w.reshape(e * n, k))
+    q, scale = quantize(w.reshape(e * n, k))
     return q.view(e, n, k), scale.view(e, n)
 
 
