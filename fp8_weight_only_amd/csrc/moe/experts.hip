@@ -67,8 +67,10 @@ __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos,
 // that, Row), the last k % 128 a masked step.
 //
 // Bound by the weight stream: one token, two of eight [14336, 4096] experts read
-// 117 MB in 22 us on 448 workgroups of eight waves, 5.3 TB/s, where a large copy
-// reaches 5.2. Measured against it: four waves the same; 32 or 16 channels per
+// 117 MB in 27.6 us on 448 workgroups of eight waves, 4.3 TB/s, when calls go
+// through all eight experts in turn (470 MB; a large copy: 4.9 to 5.2 TB/s). With
+// two pairs of experts in turn the memory-side cache (256 MB) holds part of them:
+// 22 us. Measured against those 22: four waves the same; 32 or 16 channels per
 // workgroup 23 to 25 us (more waves load the same activations); four blocks per
 // wave in flight 26, for fewer waves per CU; loads that bypass the caches 27 to
 // 30 (two lanes' 64-byte halves of a line come by separate instructions).
@@ -183,10 +185,10 @@ __global__ __launch_bounds__(W* kWave) void experts_stream_kernel(ExpertCall c, 
 // LDS to the matrix cores: every e4m3 value is a bf16 and an fp16 value.
 //
 // Two waves per SIMD and 256 x 256 tiles (128 x 64 per wave) where the rows fill
-// them: 4096 tokens, two of eight [14336, 4096] experts take 849 us, 1.1 PFLOP/s
-// with the matrix cores busy 64 % of the time at a clock of 1.94 GHz and no bank
-// conflicts; a large bf16 product of the vendor's library runs at 1.3 PFLOP/s
-// there. Raised wave priority around the products, another grouping of tiles per
+// them: 4096 tokens, two of eight [14336, 4096] experts take 838 to 871 us from
+// card to card, 1.1 PFLOP/s with the matrix cores busy 66 % of the time at a clock
+// of 1.7 to 1.9 GHz and no bank conflicts; a large bf16 product of the vendor's
+// library runs at 1.2 to 1.3 PFLOP/s there. Raised wave priority around the products, another grouping of tiles per
 // XCD (2, 8) and no stagger of k measured the same within 2 %.
 //
 // A half of a stage is 32 k: lane (i, h) takes the 16 codes and the 16 values at
@@ -568,17 +570,22 @@ ExpertPlan stream_plan(int64_t active, int64_t n, int64_t k)
 }
 
 // The plan goes by the rows per expert, were they spread evenly over as many
-// experts as can have any (how they are spread only the GPU knows). Measured on
-// [14336, 4096] x 8 and [4096, 1024] x 128 experts, us:
-//   rows per expert     1.6   4     16    32     64     128    256    1024
-//   stream              62    94    127   -      367    -      -      -
-//   256 x 32 (128 x 32) 64    88    89    117    175    366    503    -
-//   256 x 64            -     94    98    103    143    315    374    -
-//   256 x 128           -     -     123   128    129    290    317    980
-//   256 x 256           -     -     -     -      -      344    302    980
+// experts as can have any (how they are spread only the GPU knows). Measured, us,
+// rows of random tokens, weights of over 800 MB in turn:
+//                       [14336, 4096] x 8                     [4096, 1024] x 128
+//   rows per expert     4    16    32    64   128  256  1024     5    32   128
+//   stream             93   120   208   352   -    -    -       89    -     -
+//   256 x 32           88    89   118   180  268  503  1873    105   174   443
+//   128 x 32           90    94   132   202  260  472  1724     84   162   367
+//   128 x 64           93    98   104   151  218  334  1236     98   149   298
+//   256 x 64           92    95   101   138  217  334  1208    105   154   309
+//   128 x 128         109   113   121   139  216  325  1086    134   203   342
+//   256 x 128          95    99   106   126  181  305   964    110   164   279
+//   256 x 256         106   111   118   138  178  309   920    129   181   336
 // A tile's channels are halved while it leaves CUs idle; 128 x 32 where k is
-// short (several workgroups per CU then overlap their starts: 85 against 104 us
-// at k = 1024, 4 rows), 256 x 32 where it is long (89 against 96 at k = 4096).
+// short (several workgroups per CU then overlap their starts: 84 against 105 us
+// at k = 1024, 5 rows), 256 x 32 where it is long (89 against 94 at k = 4096, 16
+// rows). 128 x 128 is ahead of 128 x 64 at k = 4096 and behind it at 1024.
 // Layers too small for their tiles to fill the CUs: the stream kernel, whose
 // waves split k ([256, 14080] x 5, five rows each: 17 us against 35).
 // Rows that the ring cannot load, and k below 320 (its starts and ends are most

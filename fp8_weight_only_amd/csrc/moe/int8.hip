@@ -219,16 +219,17 @@ constexpr int kFusedK = 16384;
 // per wave are in flight. The waves' sums meet in LDS; integers, so in any order.
 //
 // FUSED (one token): the row is quantized by every workgroup for itself, into
-// LDS, behind the first weight loads: 14.0 us against 14.4 and a launch of 2.3
-// for the quantizer on [14336, 4096].
+// LDS, behind the first weight loads: 14.0 us (then) against 14.4 and a launch of
+// 2.3 for the quantizer on [14336, 4096].
 //
 // Any k and any alignment: whole blocks take 16-byte loads from any dword (below
 // that, Row), the last k % 128 a masked step.
 //
-// Bound by the weight stream: one token on [14336, 4096] (59 MB) takes 12.0 us,
-// 4.9 TB/s, in a stream of calls; two column tiles per workgroup 14.8, four
-// waves 15.3, two blocks in flight 14.9 against 14.0. From five tokens on the
-// ring below is faster where it can run: every wave here loads the tokens' codes
+// Bound by the weight stream: one token on [14336, 4096] (59 MB) takes 13.5 us, 4.4
+// TB/s, when 600 MB of weights are taken in turn, 12.0 when the memory-side cache
+// holds them. Before the first loads lost the branches between them it took 14.0
+// there; against that, two column tiles per workgroup 14.8, four waves 15.3, two
+// blocks in flight 14.9. From five tokens on the ring below is faster where it can run: every wave here loads the tokens' codes
 // for itself (16 tokens, [14336, 4096]: 16.6 us against 13.7).
 template <typename A, int RT, int CT, int W, int U, bool FUSED, bool SHIFT>
 __global__ __launch_bounds__(W* kWave) void int8_stream_kernel(Int8Call c, int TN, int TM)
@@ -638,11 +639,11 @@ __global__ __launch_bounds__(WN* WM* kWave) void int8_tile_kernel(Int8Call c, in
 // More tokens, weight rows at 16-byte boundaries, k a multiple of 64: the same
 // tiles fed by a ring of NS direct-to-LDS stages (tile.hpp).
 //
-// 4096 tokens on [14336, 4096]: 251 us, 1.9 POP/s (256 x 256 tiles, two waves per
-// SIMD; matrix cores busy 58 % of the time at 1.97 GHz, no bank conflicts), where
+// 4096 tokens on [14336, 4096]: 246 us, 2.0 POP/s (256 x 256 tiles, two waves per
+// SIMD; matrix cores busy 59 % of the time at 1.9 GHz, no bank conflicts), where
 // the register-staged tiles take 301 and the vendor's library 234. 22 tokens on
-// [4096, 14336]: 64 x 64 tiles leave 64 workgroups; k in four slices and a join
-// take 16.5 us against 33.5 in one piece.
+// [4096, 14336]: 128 x 64 tiles are 32 workgroups; k in eight slices takes 12 us
+// and the join 4, where the call without a split (fp8w_gemm_int8) takes 32.5.
 template <int BN, int BM, int WN, int WM>
 struct Int8Ring {
     static constexpr int W = WN * WM, FN = BN / WN / 32, FM = BM / WM / 32;
