@@ -2,6 +2,7 @@
 // the contract of each call are in include/fp8w_moe.h.
 #include <math.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <new>
 #include <vector>
@@ -100,6 +101,27 @@ bool expert_sizes_ok(int64_t m, int64_t e, int64_t n, int64_t k)
 {
     return dim_ok(m) && e >= 1 && e <= fp8w::kMaxExperts && dim_ok(n) && dim_ok(k) && product_ok(e, n, k) &&
            product_ok(m, n) && fp8w::tiles_fit(fp8w::max_row_tiles(m, e, 64), n);
+}
+
+int64_t fp4_bytes(int64_t k)
+{
+    return (k + 1) / 2;
+}
+
+int64_t fp4_scales(int64_t k)
+{
+    return (k + 31) / 32;
+}
+
+bool fp4_weight_ok(int64_t n, int64_t k)
+{
+    return dim_ok(n) && dim_ok(k) && product_ok(n, k);
+}
+
+bool linear_fp4_sizes_ok(int64_t m, int64_t n, int64_t k)
+{
+    return dim_ok(m) && fp4_weight_ok(n, k) && product_ok(m, n) && product_ok(m, k) &&
+           fp8w::tiles_fit((m + 63) / 64, n);
 }
 
 }  // namespace
@@ -316,6 +338,145 @@ fp8w_status_t fp8w_linear_int8(const void* x, fp8w_dtype_t act_dtype, int64_t m,
     }
     return hip_status(
         fp8w::launch_linear_int8(x, act_of(act_dtype), m, k, q, scale, bias, n, y, workspace, stream));
+}
+
+fp8w_status_t fp8w_quantize_fp4(const void* w, fp8w_dtype_t w_dtype, int64_t n, int64_t k, uint8_t* q, uint8_t* scale,
+                                hipStream_t stream)
+{
+    if (!valid_dtype(w_dtype) || !fp4_weight_ok(n, k))
+        return FP8W_ERR_INVALID_VALUE;
+    if (n == 0 || k == 0)
+        return FP8W_SUCCESS;
+    if (!w || !q || !scale)
+        return FP8W_ERR_INVALID_VALUE;
+    if (!aligned(w, elem_bytes(w_dtype)))
+        return FP8W_ERR_MISALIGNED;
+    const size_t scales = (size_t)n * (size_t)fp4_scales(k);
+    const Span sw{w, (size_t)n * (size_t)k * elem_bytes(w_dtype)}, sq{q, (size_t)n * (size_t)fp4_bytes(k)},
+        ss{scale, scales};
+    if (overlap(sw, sq) || overlap(sw, ss) || overlap(sq, ss))
+        return FP8W_ERR_INVALID_VALUE;
+    std::vector<uint8_t> host;
+    try {
+        host.resize(scales);
+    } catch (const std::bad_alloc&) {
+        return hip_status(hipErrorOutOfMemory);
+    }
+    fp8w_status_t st = hip_status(fp8w::launch_quantize_fp4(w, act_of(w_dtype), n, k, q, scale, stream));
+    if (st != FP8W_SUCCESS)
+        return st;
+    st = hip_status(fp8w::own_status(hipMemcpyAsync(host.data(), scale, scales, hipMemcpyDeviceToHost, stream)));
+    if (st != FP8W_SUCCESS)
+        return st;
+    st = hip_status(fp8w::own_status(hipStreamSynchronize(stream)));
+    if (st != FP8W_SUCCESS)
+        return st;
+    return memchr(host.data(), 255, scales) ? FP8W_ERR_NONFINITE : FP8W_SUCCESS;
+}
+
+fp8w_status_t fp8w_dequantize_fp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, void* out,
+                                  fp8w_dtype_t out_dtype, hipStream_t stream)
+{
+    if (!valid_dtype(out_dtype) || !fp4_weight_ok(n, k))
+        return FP8W_ERR_INVALID_VALUE;
+    if (n == 0 || k == 0)
+        return FP8W_SUCCESS;
+    if (!q || !scale || !out)
+        return FP8W_ERR_INVALID_VALUE;
+    if (!aligned(out, elem_bytes(out_dtype)))
+        return FP8W_ERR_MISALIGNED;
+    const Span in[] = {{q, (size_t)n * (size_t)fp4_bytes(k)}, {scale, (size_t)n * (size_t)fp4_scales(k)}};
+    if (overlaps_any({out, (size_t)n * (size_t)k * elem_bytes(out_dtype)}, in))
+        return FP8W_ERR_INVALID_VALUE;
+    return hip_status(fp8w::launch_dequantize_fp4(q, scale, n, k, out, act_of(out_dtype), stream));
+}
+
+size_t fp8w_linear_fp4_workspace_bytes(int64_t m, int64_t n, int64_t k, const void* x, const uint8_t* q,
+                                       const uint8_t* scale)
+{
+    if (!linear_fp4_sizes_ok(m, n, k) || m == 0 || n == 0)
+        return 0;
+    return fp8w::linear_fp4_workspace_bytes({m, 1, n, k, m, false}, x, q, scale);
+}
+
+const char* fp8w_linear_fp4_kernel(int64_t m, int64_t n, int64_t k, const void* x, const uint8_t* q,
+                                   const uint8_t* scale)
+{
+    if (!linear_fp4_sizes_ok(m, n, k) || m == 0 || n == 0)
+        return nullptr;
+    return fp8w::fp4_kernel_name({m, 1, n, k, m, false}, x, q, scale);
+}
+
+fp8w_status_t fp8w_linear_fp4(const void* x, fp8w_dtype_t act_dtype, int64_t m, int64_t k, const uint8_t* q,
+                              const uint8_t* scale, const void* bias, int64_t n, void* y, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream)
+{
+    if (!valid_act(act_dtype) || !linear_fp4_sizes_ok(m, n, k))
+        return FP8W_ERR_INVALID_VALUE;
+    if (m == 0 || n == 0)
+        return FP8W_SUCCESS;
+    if (!y || (k > 0 && (!x || !q || !scale)))
+        return FP8W_ERR_INVALID_VALUE;
+    if (!aligned(x, 2) || !aligned(bias, 2) || !aligned(y, 2))
+        return FP8W_ERR_MISALIGNED;
+    const Span in[] = {{x, (size_t)m * (size_t)k * 2},
+                       {q, (size_t)n * (size_t)fp4_bytes(k)},
+                       {scale, (size_t)n * (size_t)fp4_scales(k)},
+                       {bias, (size_t)n * 2}};
+    const Span out{y, (size_t)m * (size_t)n * 2};
+    if (overlaps_any(out, in))
+        return FP8W_ERR_INVALID_VALUE;
+    const size_t need = fp8w::linear_fp4_workspace_bytes({m, 1, n, k, m, false}, x, q, scale);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return FP8W_ERR_WORKSPACE;
+        if (!aligned(workspace, 16))
+            return FP8W_ERR_MISALIGNED;
+        if (overlaps_any({workspace, need}, in) || overlap({workspace, need}, out))
+            return FP8W_ERR_INVALID_VALUE;
+    }
+    const fp8w::Fp4Call c{{x, m, k, q, nullptr, bias, 1, n, nullptr, m, nullptr, nullptr, y},
+                          scale, fp4_bytes(k), fp4_scales(k), static_cast<float*>(workspace)};
+    return hip_status(fp8w::launch_fp4(c, act_of(act_dtype), stream));
+}
+
+const char* fp8w_linear_experts_fp4_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q,
+                                           const uint8_t* scale)
+{
+    if (!expert_sizes_ok(m, e, n, k) || m == 0 || n == 0)
+        return nullptr;
+    return fp8w::fp4_kernel_name({m, e, n, k, m, true}, x, q, scale);
+}
+
+fp8w_status_t fp8w_linear_experts_fp4(const void* x, fp8w_dtype_t act_dtype, int64_t x_count, int64_t k,
+                                      const uint8_t* q, const uint8_t* scale, const void* bias, int64_t e, int64_t n,
+                                      const int32_t* offsets, int64_t m, const int32_t* x_rows, const int32_t* y_rows,
+                                      void* y, hipStream_t stream)
+{
+    if (!valid_act(act_dtype) || !dim_ok(x_count) || !expert_sizes_ok(m, e, n, k) || !product_ok(x_count, k))
+        return FP8W_ERR_INVALID_VALUE;
+    if (!x_rows && x_count != m)
+        return FP8W_ERR_INVALID_VALUE;
+    if (m == 0 || n == 0)
+        return FP8W_SUCCESS;
+    if (!offsets || !y || (k > 0 && (!q || !scale || (x_count > 0 && !x))))
+        return FP8W_ERR_INVALID_VALUE;
+    if (!aligned(x, 2) || !aligned(y, 2) || !aligned(bias, 2) || !aligned(offsets, 4) || !aligned(x_rows, 4) ||
+        !aligned(y_rows, 4))
+        return FP8W_ERR_MISALIGNED;
+    const size_t rows = (size_t)e * (size_t)n;
+    const Span in[] = {{x, (size_t)x_count * (size_t)k * 2},
+                       {q, rows * (size_t)fp4_bytes(k)},
+                       {scale, rows * (size_t)fp4_scales(k)},
+                       {bias, rows * 2},
+                       {offsets, ((size_t)e + 1) * 4},
+                       {x_rows, (size_t)m * 4},
+                       {y_rows, (size_t)m * 4}};
+    if (overlaps_any({y, (size_t)m * (size_t)n * 2}, in))
+        return FP8W_ERR_INVALID_VALUE;
+    const fp8w::Fp4Call c{{x, x_count, k, q, nullptr, bias, e, n, offsets, m, x_rows, y_rows, y},
+                          scale, fp4_bytes(k), fp4_scales(k), nullptr};
+    return hip_status(fp8w::launch_fp4(c, act_of(act_dtype), stream));
 }
 
 int fp8w_moe_last_hip_error(void)

@@ -121,9 +121,10 @@ struct Row {
         return load16_part(p + (SHIFT ? shift : 0) + off, avail);
     }
     // the same for bytes() to put together: only for rows with a stage of their own
-    __device__ __forceinline__ Raw part_raw(int64_t off, int64_t avail) const
+    __device__ __forceinline__ Raw part_raw(int64_t off, int64_t avail) const { return raw(part(off, avail)); }
+    // what bytes() makes v of
+    __device__ __forceinline__ Raw raw(u32x4 v) const
     {
-        const u32x4 v = part(off, avail);
         Raw r;
         if constexpr (SHIFT) {
             // moved up by the shift that bytes() takes back

@@ -244,12 +244,76 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// linear_fp4(x, q, scale, bias, out), the workspace its own
+PyObject* linear_fp4(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Arg x, q, s;
+        Maybe b, out;
+        fp8w_dtype_t act;
+        if (n != 5 || !x.read(a[0]) || !q.read(a[1]) || !s.read(a[2]) || !b.read(a[3]) || !out.read(a[4]) ||
+            x.dim() != 2 || q.dim() != 2 || !act_type(x.type(), act))
+            return none();
+        const int64_t m = x.size(0), k = x.size(1), c = q.size(0);
+        if (!q.like(x, at::kByte, {c, (k + 1) / 2}) || !s.like(x, at::kByte, {c, (k + 31) / 32}) ||
+            !b.like(x, x.type(), {c}) || !out.like(x, x.type(), {m, c}))
+            return none();
+        const uint8_t *qp = static_cast<const uint8_t*>(q.ptr()), *sp = static_cast<const uint8_t*>(s.ptr());
+        const size_t need = fp8w_linear_fp4_workspace_bytes(m, c, k, x.ptr(), qp, sp);
+        FP8W_ON_DEVICE_OF(x);
+        const at::Tensor made = out.given ? *out.t : make(x, {m, c}, x.type());
+        at::Tensor ws;
+        if (need)
+            ws = make(x, {(int64_t)need}, at::kByte);
+        const hipStream_t stream = stream_of(x);
+        const fp8w_status_t st = without_gil([&] {
+            return fp8w_linear_fp4(x.ptr(), act, m, k, qp, sp, b.ptr(), c, made.numel() ? made.data_ptr() : nullptr,
+                                   need ? ws.data_ptr() : nullptr, need, stream);
+        });
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
+    });
+}
+
+// linear_experts_fp4(x, q, scale, offsets, bias, x_rows, y_rows, out)
+PyObject* linear_experts_fp4(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Arg x, q, s, off;
+        Maybe b, xr, yr, out;
+        fp8w_dtype_t act;
+        if (n != 8 || !x.read(a[0]) || !q.read(a[1]) || !s.read(a[2]) || !off.read(a[3]) || !b.read(a[4]) ||
+            !xr.read(a[5]) || !yr.read(a[6]) || !out.read(a[7]) || x.dim() != 2 || q.dim() != 3 ||
+            !act_type(x.type(), act))
+            return none();
+        const int64_t rows = x.size(0), k = x.size(1), e = q.size(0), c = q.size(1);
+        const int64_t m = xr.given ? xr.t->numel() : rows;
+        if (!q.like(x, at::kByte, {e, c, (k + 1) / 2}) || !s.like(x, at::kByte, {e, c, (k + 31) / 32}) ||
+            !off.like(x, at::kInt, {e + 1}) || !b.like(x, x.type(), {e, c}) || !xr.like(x, at::kInt, {m}) ||
+            !yr.like(x, at::kInt, {m}) || !out.like(x, x.type(), {m, c}))
+            return none();
+        FP8W_ON_DEVICE_OF(x);
+        const at::Tensor made = out.given ? *out.t : make(x, {m, c}, x.type());
+        const hipStream_t stream = stream_of(x);
+        const fp8w_status_t st = without_gil([&] {
+            return fp8w_linear_experts_fp4(x.ptr(), act, rows, k, static_cast<const uint8_t*>(q.ptr()),
+                                           static_cast<const uint8_t*>(s.ptr()), b.ptr(), e, c,
+                                           static_cast<const int32_t*>(off.ptr()), m,
+                                           static_cast<const int32_t*>(xr.ptr()), static_cast<const int32_t*>(yr.ptr()),
+                                           made.numel() ? made.data_ptr() : nullptr, stream);
+        });
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
+    });
+}
+
 PyMethodDef methods[] = {
     {"combine", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(combine)), METH_FASTCALL, nullptr},
     {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route)), METH_FASTCALL, nullptr},
     {"linear_experts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_experts)), METH_FASTCALL,
      nullptr},
     {"linear_int8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_int8)), METH_FASTCALL, nullptr},
+    {"linear_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_fp4)), METH_FASTCALL, nullptr},
+    {"linear_experts_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_experts_fp4)),
+     METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_helpers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -89,6 +89,27 @@ struct ExpertCall {
 hipError_t launch_experts(const ExpertCall& c, Act act, hipStream_t stream);
 const char* experts_kernel_name(int64_t m, int64_t e, int64_t n, int64_t k, const void* x, const uint8_t* q);
 
+// The same on 4-bit weights: q rows of row_bytes = (k + 1) / 2 bytes, row_scales =
+// (k + 31) / 32 e8m0 scales of a row, no scale of a channel. Without offsets e == 1
+// and all rows are that expert's.
+struct Fp4Call : ExpertCall {
+    const uint8_t* block_scale;
+    int64_t row_bytes, row_scales;
+    float* parts;  // the linear layer's workspace, where its plan needs one
+};
+struct Fp4Shape {
+    int64_t m, e, n, k, xr;
+    bool grouped;
+    int64_t row_tiles(int64_t bm) const { return grouped ? max_row_tiles(m, e, bm) : (m + bm - 1) / bm; }
+};
+hipError_t launch_fp4(const Fp4Call& c, Act act, hipStream_t stream);
+size_t linear_fp4_workspace_bytes(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale);
+const char* fp4_kernel_name(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale);
+hipError_t launch_quantize_fp4(const void* w, Act type, int64_t n, int64_t k, uint8_t* q, uint8_t* scale,
+                               hipStream_t stream);
+hipError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, void* out, Act type,
+                                 hipStream_t stream);
+
 // qx rows are kx >= k bytes apart (kx > k: bytes k .. kx - 1 of every row are
 // written as zeros).
 hipError_t launch_quantize_int8(const void* x, Act type, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale,

@@ -37,6 +37,11 @@ struct Rows {
     {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, FP8W_LDS(dst), 16, lane_off, off, 0, 0);
     }
+    // 4 bytes per lane, at dst + 4 * lane
+    __device__ __forceinline__ void load4(int lane_off, int off, uint8_t* dst) const
+    {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, FP8W_LDS(dst), 4, lane_off, off, 0, 0);
+    }
 };
 
 // Workgroup barrier behind which LDS writes before it are seen; loads into

@@ -1,4 +1,4 @@
-"""Mixture-of-experts operators and the int8 linear layer.
+"""Mixture-of-experts operators, and the int8 and 4-bit linear layers.
 
 A thin ctypes binding over ``libfp8w_moe.so`` (declared in
 ``include/fp8w_moe.h``), in the manner of the package's FP8 linear layer: the
@@ -17,9 +17,14 @@ CPU or PyTorch fallback.
 
     q, scale = quantize_int8(w)                    # build time
     y = linear_int8(x, q, scale, bias)             # x quantized per token in the call
+
+    q, scale = quantize_fp4(w)                     # build time; w [n, k], or [e, n, k] for experts
+    y = linear_fp4(x, q, scale, bias)
+    h = linear_experts_fp4(x, qe, se, r.offsets, x_rows=r.tokens)
 """
 import contextlib
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -44,12 +49,20 @@ MOE_EXPORTS = {
     "fp8w_linear_int8": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
     "fp8w_linear_int8_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _P]),
     "fp8w_linear_int8_kernel": (ctypes.c_char_p, [_I64, _I64, _I64, _P, _P]),
+    "fp8w_quantize_fp4": (_I, [_P, _I, _I64, _I64, _P, _P, _P]),
+    "fp8w_dequantize_fp4": (_I, [_P, _P, _I64, _I64, _P, _I, _P]),
+    "fp8w_linear_fp4": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "fp8w_linear_fp4_workspace_bytes": (_SZ, [_I64, _I64, _I64, _P, _P, _P]),
+    "fp8w_linear_fp4_kernel": (ctypes.c_char_p, [_I64, _I64, _I64, _P, _P, _P]),
+    "fp8w_linear_experts_fp4": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P]),
+    "fp8w_linear_experts_fp4_kernel": (ctypes.c_char_p, [_I64, _I64, _I64, _I64, _P, _P, _P]),
     "fp8w_moe_last_hip_error": (_I, []),
 }
 
 __all__ = [*MOE_EXPORTS, "MOE_EXPORTS", "Fp8wMoeError", "moe_lib_path", "load_moe", "Route", "route",
            "quantize_experts", "linear_experts", "experts_workspace_bytes", "combine", "quantize_int8",
-           "quantize_activations_int8", "gemm_int8", "linear_int8", "int8_workspace_bytes"]
+           "quantize_activations_int8", "gemm_int8", "linear_int8", "int8_workspace_bytes", "quantize_fp4",
+           "dequantize_fp4", "linear_fp4", "fp4_workspace_bytes", "linear_experts_fp4"]
 
 _LIB = None
 _FAST = None
@@ -142,6 +155,38 @@ def fp8w_linear_int8_workspace_bytes(m, n, k, x, q) -> int:
 
 def fp8w_linear_int8_kernel(m, n, k, x, q):
     r = load_moe().fp8w_linear_int8_kernel(m, n, k, x, q)
+    return r.decode() if r is not None else None
+
+
+def fp8w_quantize_fp4(w, w_dtype, n, k, q, scale, stream) -> int:
+    return load_moe().fp8w_quantize_fp4(w, w_dtype, n, k, q, scale, stream)
+
+
+def fp8w_dequantize_fp4(q, scale, n, k, out, out_dtype, stream) -> int:
+    return load_moe().fp8w_dequantize_fp4(q, scale, n, k, out, out_dtype, stream)
+
+
+def fp8w_linear_fp4(x, act_dtype, m, k, q, scale, bias, n, y, workspace, workspace_bytes, stream) -> int:
+    return load_moe().fp8w_linear_fp4(x, act_dtype, m, k, q, scale, bias, n, y, workspace, workspace_bytes, stream)
+
+
+def fp8w_linear_fp4_workspace_bytes(m, n, k, x, q, scale) -> int:
+    return load_moe().fp8w_linear_fp4_workspace_bytes(m, n, k, x, q, scale)
+
+
+def fp8w_linear_fp4_kernel(m, n, k, x, q, scale):
+    r = load_moe().fp8w_linear_fp4_kernel(m, n, k, x, q, scale)
+    return r.decode() if r is not None else None
+
+
+def fp8w_linear_experts_fp4(x, act_dtype, x_count, k, q, scale, bias, e, n, offsets, m, x_rows, y_rows, y,
+                            stream) -> int:
+    return load_moe().fp8w_linear_experts_fp4(x, act_dtype, x_count, k, q, scale, bias, e, n, offsets, m, x_rows,
+                                              y_rows, y, stream)
+
+
+def fp8w_linear_experts_fp4_kernel(m, e, n, k, x, q, scale):
+    r = load_moe().fp8w_linear_experts_fp4_kernel(m, e, n, k, x, q, scale)
     return r.decode() if r is not None else None
 
 
@@ -430,4 +475,115 @@ def linear_int8(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: tor
     with _on(dev):
         st = fp8w_linear_int8(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, _stream(dev))
     _check(st, "fp8w_linear_int8")
+    return out
+
+
+def quantize_fp4(w: torch.Tensor):
+    """4-bit quantization of a weight [n, k], or of a stack of experts' [e, n, k]
+    (fp32, bf16 or fp16): (q uint8 [.., n, (k + 1) // 2], two e2m1 codes to a byte,
+    the even k in the low four bits; scale uint8 [.., n, (k + 31) // 32], one
+    power of two 2^(s - 127) for 32 weights). Synchronizes; raises Fp8wMoeError on
+    NaN / inf weights."""
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [n, k] or [e, n, k]")
+    dev = _gpu(w, "w", w.dim())
+    lead, n, k = w.shape[:-1], math.prod(w.shape[:-1]), w.shape[-1]
+    if w.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {w.dtype}")
+    q = torch.empty((*lead, (k + 1) // 2), dtype=torch.uint8, device=dev)
+    scale = torch.empty((*lead, (k + 31) // 32), dtype=torch.uint8, device=dev)
+    wp = _want(w, "w", w.shape, w.dtype, dev)
+    with _on(dev):
+        st = fp8w_quantize_fp4(wp, _DT[w.dtype], n, k, q.data_ptr() if q.numel() else 0,
+                               scale.data_ptr() if scale.numel() else 0, _stream(dev))
+    _check(st, "fp8w_quantize_fp4")
+    return q, scale
+
+
+def dequantize_fp4(q: torch.Tensor, scale: torch.Tensor, k: int = None,
+                   dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """The weights [.., n, k] of ``quantize_fp4``'s codes and scales (k: 2 q.shape[-1]
+    unless given) in ``dtype``: exact in fp32 and bf16, rounded once in fp16."""
+    if q.dim() not in (2, 3):
+        raise ValueError("q must have 2 or 3 dimensions")
+    dev = _gpu(q, "q", q.dim())
+    k = 2 * q.shape[-1] if k is None else k
+    lead, n = q.shape[:-1], math.prod(q.shape[:-1])
+    if (k + 1) // 2 != q.shape[-1]:
+        raise ValueError("k must be 2 q.shape[-1] or one less")
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    qp = _want(q, "q", q.shape, torch.uint8, dev)
+    sp = _want(scale, "scale", (*lead, (k + 31) // 32), torch.uint8, dev)
+    out = torch.empty((*lead, k), dtype=dtype, device=dev)
+    with _on(dev):
+        st = fp8w_dequantize_fp4(qp, sp, n, k, out.data_ptr() if out.numel() else 0, _DT[dtype], _stream(dev))
+    _check(st, "fp8w_dequantize_fp4")
+    return out
+
+
+def fp4_workspace_bytes(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor) -> int:
+    return fp8w_linear_fp4_workspace_bytes(x.shape[0], q.shape[0], x.shape[1], x.data_ptr(), q.data_ptr(),
+                                           scale.data_ptr())
+
+
+def linear_fp4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor = None,
+               out: torch.Tensor = None, workspace: torch.Tensor = None) -> torch.Tensor:
+    """y = x @ w.T + bias on 4-bit weights, fp32 sums, rounded once to x.dtype.
+
+    x: [m, k] bf16 / fp16, any m; q: [n, (k + 1) // 2] uint8 and scale: [n, (k + 31)
+    // 32] uint8 as ``quantize_fp4`` gives them; bias: [n] of x.dtype. In fp16 a
+    weight is its fp16 value (exact for scales 2^-23 .. 2^13)."""
+    if workspace is None:
+        r = (_FAST or _fast()).linear_fp4(x, q, scale, bias, out)
+        if r is not None:
+            return r if type(r) is not int else _check(r, "fp8w_linear_fp4")
+    dev = _gpu(x, "x", 2)
+    if q.dim() != 2:
+        raise ValueError("q must have 2 dimensions")
+    m, k = x.shape
+    n = q.shape[0]
+    act = _act_code(x.dtype, "x")
+    xp = _want(x, "x", (m, k), x.dtype, dev)
+    qp = _want(q, "q", (n, (k + 1) // 2), torch.uint8, dev)
+    sp = _want(scale, "scale", (n, (k + 31) // 32), torch.uint8, dev)
+    bp = _want(bias, "bias", (n,), x.dtype, dev)
+    if out is None:
+        out = x.new_empty((m, n))
+    yp = _want(out, "out", (m, n), x.dtype, dev)
+    workspace, wp, wb = _workspace(workspace, fp8w_linear_fp4_workspace_bytes(m, n, k, xp, qp, sp), dev)
+    with _on(dev):
+        st = fp8w_linear_fp4(xp, act, m, k, qp, sp, bp, n, yp, wp, wb, _stream(dev))
+    _check(st, "fp8w_linear_fp4")
+    return out
+
+
+def linear_experts_fp4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, offsets: torch.Tensor,
+                       bias: torch.Tensor = None, x_rows: torch.Tensor = None, y_rows: torch.Tensor = None,
+                       out: torch.Tensor = None) -> torch.Tensor:
+    """``linear_experts`` on 4-bit weights: q [e, n, (k + 1) // 2] uint8 and scale
+    [e, n, (k + 31) // 32] uint8 as ``quantize_fp4`` gives them for [e, n, k]."""
+    r = (_FAST or _fast()).linear_experts_fp4(x, q, scale, offsets, bias, x_rows, y_rows, out)
+    if r is not None:
+        return r if type(r) is not int else _check(r, "fp8w_linear_experts_fp4")
+    dev = _gpu(x, "x", 2)
+    if q.dim() != 3:
+        raise ValueError("q must have 3 dimensions")
+    rows, k = x.shape
+    e, n = q.shape[:2]
+    m = rows if x_rows is None else x_rows.numel()
+    act = _act_code(x.dtype, "x")
+    xp = _want(x, "x", (rows, k), x.dtype, dev)
+    qp = _want(q, "q", (e, n, (k + 1) // 2), torch.uint8, dev)
+    sp = _want(scale, "scale", (e, n, (k + 31) // 32), torch.uint8, dev)
+    bp = _want(bias, "bias", (e, n), x.dtype, dev)
+    op = _want(offsets, "offsets", (e + 1,), torch.int32, dev)
+    ip = _want(x_rows, "x_rows", (m,), torch.int32, dev)
+    jp = _want(y_rows, "y_rows", (m,), torch.int32, dev)
+    if out is None:
+        out = x.new_empty((m, n))
+    yp = _want(out, "out", (m, n), x.dtype, dev)
+    with _on(dev):
+        st = fp8w_linear_experts_fp4(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, _stream(dev))
+    _check(st, "fp8w_linear_experts_fp4")
     return out

@@ -1,14 +1,14 @@
 /*
- * fp8w_moe — mixture-of-experts operators and the int8 linear layer for AMD
- * MI355X (gfx950), next to the FP8 weight-only linear layer of fp8w.h.
+ * fp8w_moe — mixture-of-experts operators and the int8 and 4-bit linear layers for
+ * AMD MI355X (gfx950), next to the FP8 weight-only linear layer of fp8w.h.
  *
  * C ABI of libfp8w_moe.so. The conventions are those of fp8w.h: dense row-major
  * tensors, device pointers owned by the caller, no allocation by the library,
  * work enqueued on `stream` (0 = the null stream) in stream order, arguments
  * validated before anything is enqueued, status codes and dtypes of fp8w.h. The
  * thread's current device is the buffers' and the stream's. Every call is
- * asynchronous and can be captured into a HIP graph, but for fp8w_quantize_int8,
- * which synchronizes. A call's results depend on its arguments alone (no order of
+ * asynchronous and can be captured into a HIP graph, but for fp8w_quantize_int8 and
+ * fp8w_quantize_fp4, which synchronize. A call's results depend on its arguments alone (no order of
  * atomics enters them). Inputs may be read by whole aligned dwords, that is with
  * up to three bytes beside their first and last. Sizes up to 2^31 - 1 unless
  * stated; a call whose products or sums would need a launch of 2^32 threads or
@@ -139,6 +139,68 @@ FP8W_API size_t fp8w_linear_int8_workspace_bytes(int64_t m, int64_t n, int64_t k
 
 /* Names of the kernels fp8w_linear_int8 runs; NULL as for experts. */
 FP8W_API const char* fp8w_linear_int8_kernel(int64_t m, int64_t n, int64_t k, const void* x, const int8_t* q);
+
+/*
+ * 4-bit weights: e2m1 codes (sign, two bits of exponent, one of mantissa: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6) with one e8m0 scale 2^(s - 127) for a block of 32 along k, the
+ * OCP MX format of that element type.
+ *   q      [n, (k + 1) / 2] bytes: an even k's code in the low four bits, the next
+ *          one's in the high four (those of an odd row's last byte are ignored).
+ *   scale  [n, (k + 31) / 32] bytes s; the last block of a row may be shorter. 255
+ *          makes the block's weights NaN.
+ * A weight enters a product as its value in the activation type: exact in BF16 for
+ * every scale; in FP16 exact for scales 2^-23 .. 2^13, beyond them rounded as FP16
+ * rounds (to its subnormals, or to infinity above 65504).
+ */
+
+/*
+ * Build-time quantizer of w [n, k] (BF16, FP16 or FP32): s = floor(log2(amax)) - 2 +
+ * 127 of each block (0 for a block below 2^-124 or of zeros), codes the nearest
+ * values of w / 2^(s - 127), ties to the even code, those beyond 6 the code of 6.
+ * Synchronizes; FP8W_ERR_NONFINITE when a weight is NaN or infinite (its block then
+ * has s == 255). k <= 2^31 - 1. No two buffers may overlap.
+ */
+FP8W_API fp8w_status_t fp8w_quantize_fp4(const void* w, fp8w_dtype_t w_dtype, int64_t n, int64_t k, uint8_t* q,
+                                         uint8_t* scale, hipStream_t stream);
+
+/* The weights [n, k] of codes and scales, rounded once to out_dtype (exact in FP32
+ * and BF16). */
+FP8W_API fp8w_status_t fp8w_dequantize_fp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, void* out,
+                                           fp8w_dtype_t out_dtype, hipStream_t stream);
+
+/*
+ * The linear layer on 4-bit weights:
+ *   y[t, c] = sum_k x[t, k] * w[c, k] + bias[c]
+ * in fp32, rounded once to act_dtype (BF16 or FP16). x [m, k], bias [n] of act_dtype
+ * or NULL, y [m, n]; y must not overlap an input. workspace of
+ * fp8w_linear_fp4_workspace_bytes bytes, 16-byte aligned (FP8W_ERR_WORKSPACE when
+ * short), for the calls that split k over workgroups.
+ */
+FP8W_API fp8w_status_t fp8w_linear_fp4(const void* x, fp8w_dtype_t act_dtype, int64_t m, int64_t k, const uint8_t* q,
+                                       const uint8_t* scale, const void* bias, int64_t n, void* y, void* workspace,
+                                       size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of fp8w_linear_fp4 for these sizes and pointers (NULL: aligned);
+ * 0 for invalid sizes. */
+FP8W_API size_t fp8w_linear_fp4_workspace_bytes(int64_t m, int64_t n, int64_t k, const void* x, const uint8_t* q,
+                                                const uint8_t* scale);
+
+/* Name of the kernel fp8w_linear_fp4 runs; NULL as for experts. */
+FP8W_API const char* fp8w_linear_fp4_kernel(int64_t m, int64_t n, int64_t k, const void* x, const uint8_t* q,
+                                            const uint8_t* scale);
+
+/*
+ * fp8w_linear_experts on 4-bit weights: q [e, n, (k + 1) / 2], scale [e, n, (k + 31) /
+ * 32]; everything else as there. No workspace.
+ */
+FP8W_API fp8w_status_t fp8w_linear_experts_fp4(const void* x, fp8w_dtype_t act_dtype, int64_t x_count, int64_t k,
+                                               const uint8_t* q, const uint8_t* scale, const void* bias, int64_t e,
+                                               int64_t n, const int32_t* offsets, int64_t m, const int32_t* x_rows,
+                                               const int32_t* y_rows, void* y, hipStream_t stream);
+
+/* Name of its kernel, as fp8w_linear_experts_kernel. */
+FP8W_API const char* fp8w_linear_experts_fp4_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
+                                                    const uint8_t* q, const uint8_t* scale);
 
 /* The hipError_t behind this thread's last FP8W_ERR_HIP of this library. */
 FP8W_API int fp8w_moe_last_hip_error(void);
