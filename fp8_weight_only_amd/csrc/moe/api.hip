@@ -124,6 +124,21 @@ bool linear_fp4_sizes_ok(int64_t m, int64_t n, int64_t k)
            fp8w::tiles_fit((m + 63) / 64, n);
 }
 
+bool layer_sizes_ok(int64_t t, int64_t e, int64_t top, int64_t hidden, int64_t inner)
+{
+    return t >= 0 && t <= fp8w::kMaxLayerTokens && route_sizes_ok(t, e, top) && hidden >= 1 &&
+           hidden <= fp8w::kMaxLayerWidth && inner >= 1 && inner <= fp8w::kMaxLayerWidth;
+}
+
+struct WeightBytes {
+    size_t q, scale, bias;
+    WeightBytes(fp8w_weight_format_t format, int64_t rows, int64_t k)
+        : q((size_t)rows * (size_t)(format == FP8W_WEIGHT_FP4 ? fp4_bytes(k) : k)),
+          scale((size_t)rows * (size_t)(format == FP8W_WEIGHT_FP4 ? fp4_scales(k) : 4)), bias((size_t)rows * 2)
+    {
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -477,6 +492,62 @@ fp8w_status_t fp8w_linear_experts_fp4(const void* x, fp8w_dtype_t act_dtype, int
     const fp8w::Fp4Call c{{x, x_count, k, q, nullptr, bias, e, n, offsets, m, x_rows, y_rows, y},
                           scale, fp4_bytes(k), fp4_scales(k), nullptr};
     return hip_status(fp8w::launch_fp4(c, act_of(act_dtype), stream));
+}
+
+size_t fp8w_moe_layer_workspace_bytes(int64_t t, int64_t e, int64_t top_k, int64_t hidden, int64_t inner)
+{
+    return layer_sizes_ok(t, e, top_k, hidden, inner) && t > 0 ? fp8w::layer_workspace_bytes(t, top_k, inner) : 0;
+}
+
+fp8w_status_t fp8w_moe_layer(const void* x, fp8w_dtype_t act_dtype, int64_t t, int64_t hidden, const void* logits,
+                             fp8w_dtype_t logits_dtype, int64_t e, int64_t top_k, int renormalize,
+                             fp8w_weight_format_t format, const uint8_t* q_gate_up, const void* scale_gate_up,
+                             const void* bias_gate_up, int64_t inner, const uint8_t* q_down, const void* scale_down,
+                             const void* bias_down, void* out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream)
+{
+    if (!valid_act(act_dtype) || !valid_dtype(logits_dtype) || !layer_sizes_ok(t, e, top_k, hidden, inner) ||
+        (format != FP8W_WEIGHT_E4M3 && format != FP8W_WEIGHT_FP4))
+        return FP8W_ERR_INVALID_VALUE;
+    if (t == 0)
+        return FP8W_SUCCESS;
+    if (!x || !logits || !q_gate_up || !scale_gate_up || !q_down || !scale_down || !out)
+        return FP8W_ERR_INVALID_VALUE;
+    const uintptr_t scale_align = format == FP8W_WEIGHT_FP4 ? 1 : 4;
+    if (!aligned(x, 2) || !aligned(logits, elem_bytes(logits_dtype)) || !aligned(scale_gate_up, scale_align) ||
+        !aligned(bias_gate_up, 2) || !aligned(scale_down, scale_align) || !aligned(bias_down, 2) || !aligned(out, 2))
+        return FP8W_ERR_MISALIGNED;
+    const size_t need = fp8w::layer_workspace_bytes(t, top_k, inner), tokens = (size_t)t * (size_t)hidden * 2;
+    if (!workspace || workspace_bytes < need)
+        return FP8W_ERR_WORKSPACE;
+    if (!aligned(workspace, 16))
+        return FP8W_ERR_MISALIGNED;
+    const WeightBytes up(format, 2 * e * inner, hidden), down(format, e * hidden, inner);
+    const Span in[] = {{x, tokens},
+                       {logits, (size_t)t * (size_t)e * elem_bytes(logits_dtype)},
+                       {q_gate_up, up.q},
+                       {scale_gate_up, up.scale},
+                       {bias_gate_up, up.bias},
+                       {q_down, down.q},
+                       {scale_down, down.scale},
+                       {bias_down, down.bias}};
+    const Span to{out, tokens}, ws{workspace, need};
+    if (overlaps_any(to, in) || overlaps_any(ws, in) || overlap(to, ws))
+        return FP8W_ERR_INVALID_VALUE;
+    fp8w::LayerCall c{};
+    c.x = x;
+    c.logits = logits;
+    c.logits_type = act_of(logits_dtype);
+    c.top = (int)top_k;
+    c.renorm = renormalize != 0;
+    c.t = t;
+    c.e = e;
+    c.hidden = hidden;
+    c.inner = inner;
+    c.up = {q_gate_up, scale_gate_up, bias_gate_up};
+    c.down = {q_down, scale_down, bias_down};
+    c.out = out;
+    return hip_status(fp8w::launch_layer(c, format == FP8W_WEIGHT_FP4, act_of(act_dtype), workspace, stream));
 }
 
 int fp8w_moe_last_hip_error(void)

@@ -305,6 +305,62 @@ PyObject* linear_experts_fp4(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// moe_layer(x, logits, top_k, (q, scale), (q, scale), gate_up_bias, down_bias, renormalize, out), the workspace its own
+PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        Arg x, l, q[2], s[2];
+        Maybe b[2], out;
+        fp8w_dtype_t act;
+        if (n != 9 || !x.read(a[0]) || !l.read(a[1]) || !PyLong_CheckExact(a[2]) || !b[0].read(a[5]) || !b[1].read(a[6]) ||
+            !out.read(a[8]) || x.dim() != 2 || l.dim() != 2 || !act_type(x.type(), act))
+            return none();
+        for (int i = 0; i < 2; ++i) {
+            PyObject* pair = a[3 + i];
+            if (!PyTuple_Check(pair) || PyTuple_GET_SIZE(pair) != 2 || !q[i].read(PyTuple_GET_ITEM(pair, 0)) ||
+                !s[i].read(PyTuple_GET_ITEM(pair, 1)) || q[i].dim() != 3)
+                return none();
+        }
+        const int64_t t = x.size(0), hidden = x.size(1), e = l.size(1), inner = q[0].size(1) / 2;
+        const long long top = PyLong_AsLongLong(a[2]);
+        if (top == -1 && PyErr_Occurred()) {
+            PyErr_Clear();
+            return none();
+        }
+        const int renorm = PyObject_IsTrue(a[7]);
+        const at::ScalarType type = l.type();
+        const fp8w_dtype_t dt = type == at::kBFloat16 ? FP8W_BF16 : (type == at::kHalf ? FP8W_FP16 : FP8W_FP32);
+        const bool fp4 = s[0].type() == at::kByte;
+        if (renorm < 0 || (dt == FP8W_FP32 && type != at::kFloat) || !l.like(x, type, {t, e}))
+            return none();
+        const int64_t rows[2] = {2 * inner, hidden}, k[2] = {hidden, inner};
+        for (int i = 0; i < 2; ++i)
+            if (!q[i].like(x, at::kByte, {e, rows[i], fp4 ? (k[i] + 1) / 2 : k[i]}) ||
+                !(fp4 ? s[i].like(x, at::kByte, {e, rows[i], (k[i] + 31) / 32}) : s[i].like(x, at::kFloat, {e, rows[i]})) ||
+                !b[i].like(x, x.type(), {e, rows[i]}))
+                return none();
+        if (!out.like(x, x.type(), {t, hidden}))
+            return none();
+        const size_t need = fp8w_moe_layer_workspace_bytes(t, e, top, hidden, inner);
+        if (t > 0 && need == 0)
+            return none();  // sizes that the call does not take
+        FP8W_ON_DEVICE_OF(x);
+        const at::Tensor made = out.given ? *out.t : make(x, {t, hidden}, x.type());
+        at::Tensor ws;
+        if (need)
+            ws = make(x, {(int64_t)need}, at::kByte);
+        const hipStream_t stream = stream_of(x);
+        const fp8w_status_t st = without_gil([&] {
+            return fp8w_moe_layer(x.ptr(), act, t, hidden, l.ptr(), dt, e, top, renorm,
+                                  fp4 ? FP8W_WEIGHT_FP4 : FP8W_WEIGHT_E4M3, static_cast<const uint8_t*>(q[0].ptr()),
+                                  s[0].ptr(), b[0].ptr(), inner, static_cast<const uint8_t*>(q[1].ptr()), s[1].ptr(),
+                                  b[1].ptr(), made.numel() ? made.data_ptr() : nullptr, need ? ws.data_ptr() : nullptr,
+                                  need, stream);
+        });
+        return st == FP8W_SUCCESS ? THPVariable_Wrap(made) : failed(st);
+    });
+}
+
 PyMethodDef methods[] = {
     {"combine", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(combine)), METH_FASTCALL, nullptr},
     {"route", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route)), METH_FASTCALL, nullptr},
@@ -314,6 +370,7 @@ PyMethodDef methods[] = {
     {"linear_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_fp4)), METH_FASTCALL, nullptr},
     {"linear_experts_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear_experts_fp4)),
      METH_FASTCALL, nullptr},
+    {"moe_layer", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(moe_layer)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_helpers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -110,6 +110,31 @@ hipError_t launch_quantize_fp4(const void* w, Act type, int64_t n, int64_t k, ui
 hipError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* scale, int64_t n, int64_t k, void* out, Act type,
                                  hipStream_t stream);
 
+constexpr int kMaxLayerTokens = 64;
+constexpr int64_t kMaxLayerWidth = (int64_t)1 << 22;  // blocks of k times experts fit an int
+
+struct LayerWeights {
+    const uint8_t* q;
+    const void* scale;  // [e, n] fp32 of e4m3 codes, [e, n, (k + 31) / 32] bytes of 4-bit ones
+    const void* bias;   // [e, n] or null
+};
+struct LayerCall {
+    const void* x;  // [t, hidden]
+    const void* logits;
+    Act logits_type;
+    int top, renorm;
+    int64_t t, e, hidden, inner;
+    LayerWeights up, down;  // [e, 2 inner, hidden], [e, hidden, inner]
+    void* out;
+    // the workspace's parts, set by launch_layer
+    int32_t* ids;
+    float* weights;
+    uint16_t* h;
+    int64_t pitch;
+};
+size_t layer_workspace_bytes(int64_t t, int64_t top, int64_t inner);
+hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t stream);
+
 // qx rows are kx >= k bytes apart (kx > k: bytes k .. kx - 1 of every row are
 // written as zeros).
 hipError_t launch_quantize_int8(const void* x, Act type, int64_t rows, int64_t k, int8_t* q, int64_t kx, float* scale,

@@ -12,13 +12,7 @@
 //                  number of slots with an expert
 //   tokens         slots / top
 //
-// Choice: G lanes hold a token (64, or 16 where e <= 64 and top <= 16: four
-// tokens per wave), J consecutive experts each. A logit becomes an unsigned key
-// of the same order (NaN above everything, both zeros equal, -inf key 0 = not to
-// be taken). A round is an integer maximum over registers and lanes (DPP
-// rotations within rows of 16 lanes, row swaps across them), the first lane and
-// register that hold it (the lowest index, since a lane's experts are
-// consecutive), and that key cleared.
+// Choice: choose.hpp.
 //
 // Order: a counting sort without atomics on global memory, so the lists do not
 // depend on timing. Tokens are cut into at most 256 chunks; the first kernel
@@ -33,10 +27,7 @@
 // bound by vector instructions (one more choice of 32768 costs 1.9 us; with one,
 // 11), the order by its chain of short steps (8 us for 4096 tokens). One token, 8
 // of 128: 5.1 us in its launch, where a launch with little to do takes 2.
-#include <math.h>
-
-#include "device.hpp"
-#include "moe.hpp"
+#include "choose.hpp"
 
 namespace fp8w {
 namespace {
@@ -44,258 +35,6 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kChunks = 256;
-
-__device__ __forceinline__ uint32_t key_of(float f)
-{
-    const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 becomes 0
-    uint32_t key = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-    key = f == -INFINITY ? 0 : key;
-    return f != f ? 0xffffffffu : key;
-}
-
-// the logit of a key (a NaN for a NaN's key, -inf for key 0)
-__device__ __forceinline__ float logit_of(uint32_t key)
-{
-    if (key == 0)
-        return -INFINITY;
-    return __builtin_bit_cast(float, (key >> 31) ? key ^ 0x80000000u : ~key);
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t rotated(uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-}
-
-// OP over the G lanes of a group, in all of them.
-template <int G, typename OP>
-__device__ __forceinline__ uint32_t group_reduce(uint32_t v, OP op)
-{
-    static_assert(G == 16 || G == 64, "a row of lanes or the wave");
-    v = op(v, rotated<0x128>(v));  // row_ror:8
-    v = op(v, rotated<0x124>(v));
-    v = op(v, rotated<0x122>(v));
-    v = op(v, rotated<0x121>(v));
-    if constexpr (G == 64) {
-        const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);  // even rows' and odd rows' values
-        v = op(a[0], a[1]);
-        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        v = op(b[0], b[1]);
-    }
-    return v;
-}
-
-template <int G>
-__device__ __forceinline__ uint32_t group_max(uint32_t v)
-{
-    if constexpr (G == 64)
-        return wave_max_u32(v);  // in a scalar register
-    else
-        return group_reduce<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-}
-
-template <int G>
-__device__ __forceinline__ float group_sum(float v)
-{
-    return __builtin_bit_cast(float, group_reduce<G>(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
-                                  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) +
-                                                                          __builtin_bit_cast(float, b));
-                              }));
-}
-
-// A lane's J logits of a row, -inf past its end.
-template <int J>
-__device__ __forceinline__ void load_logits(const void* logits, Act type, int64_t row, int e, int first, float* l)
-{
-    if (type == Act::FP32) {
-        const float* p = static_cast<const float*>(logits) + row * e + first;
-        if (J == 4 && first + 4 <= e) {
-            const u32x4 v = load16_any(p);
-            const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                l[j] = __builtin_bit_cast(float, d[j & 3]);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            l[j] = first + j < e ? p[j] : -INFINITY;
-        return;
-    }
-    const uint16_t* p = static_cast<const uint16_t*>(logits) + row * e + first;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const uint16_t b = first + j < e ? p[j] : (uint16_t)0;
-        const float f = type == Act::BF16 ? Bf16::to_f32(b) : F16::to_f32(b);
-        l[j] = first + j < e ? f : -INFINITY;
-    }
-}
-
-// A group's next choice: the largest key left among its lanes' (0: none left),
-// taken out, and its expert. A lane's keys are sorted where they are few (a
-// choice is then its first key, and taking it a shift), else searched each time.
-template <int G, int J>
-struct Keys {
-    static constexpr bool kSorted = J <= 4;
-    uint32_t key[J];
-    uint32_t order;  // sorted: the registers' original numbers, a byte each, first key's lowest
-
-    __device__ __forceinline__ explicit Keys(const float (&l)[J])
-    {
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-            key[j] = key_of(l[j]);
-        if constexpr (kSorted) {
-            uint32_t id[J];
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                id[j] = j;
-            // neighbours exchanged only where the later is larger: equal keys stay in order
-#pragma unroll
-            for (int n = J - 1; n >= 1; --n)
-#pragma unroll
-                for (int j = 0; j < n; ++j) {
-                    const bool swap = key[j + 1] > key[j];
-                    const uint32_t hi = swap ? key[j + 1] : key[j], lo = swap ? key[j] : key[j + 1];
-                    const uint32_t a = swap ? id[j + 1] : id[j], b = swap ? id[j] : id[j + 1];
-                    key[j] = hi;
-                    key[j + 1] = lo;
-                    id[j] = a;
-                    id[j + 1] = b;
-                }
-            order = 0;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                order |= id[j] << (8 * j);
-        }
-    }
-
-    __device__ __forceinline__ uint32_t take(int& expert)
-    {
-        const int lane = threadIdx.x & 63, in = lane % G;
-        uint32_t head = key[0];
-        int at = 0;
-        if constexpr (kSorted) {
-            at = (int)(order & 255u);
-        } else {
-#pragma unroll
-            for (int j = 1; j < J; ++j)
-                head = head > key[j] ? head : key[j];
-#pragma unroll
-            for (int j = J - 1; j >= 1; --j)
-                at = key[j] == head ? j : at;
-            at = key[0] == head ? 0 : at;
-        }
-        const uint32_t best = group_max<G>(head);
-        bool mine;
-        if constexpr (G == 64) {
-            const int win = (int)__builtin_ctzll(__ballot(head == best));  // never empty
-            expert = __builtin_amdgcn_readlane(at, win) + win * J;
-            mine = lane == win;
-        } else {
-            expert = (int)group_reduce<G>(head == best ? (uint32_t)(in * J + at) : 0xffffffffu,
-                                          [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-            mine = expert / J == in;
-        }
-        if constexpr (kSorted) {
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                key[j] = mine ? (j + 1 < J ? key[j + 1 < J ? j + 1 : j] : 0) : key[j];
-            order = mine ? order >> 8 : order;
-        } else {
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                key[j] = mine && j == at ? 0 : key[j];
-        }
-        return best;
-    }
-};
-
-// Two tokens per group at a time (their chains of dependent steps overlap), from
-// l[u][j], the token's logit of expert in * J + j. Lane r of a group gets its
-// tokens' r-th choice in id[u] (-1: none) and its weight.
-template <int G, int J, int U>
-__device__ __forceinline__ void choose(const float (&l)[U][J], int top, bool renorm, float (&weight)[U], int (&id)[U])
-{
-    static_assert(U == 2, "two tokens");
-    const int in = (threadIdx.x & 63) % G;
-    uint32_t mine[U], peak[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        mine[u] = peak[u] = 0;
-        id[u] = -1;
-    }
-    Keys<G, J> keys[U] = {Keys<G, J>(l[0]), Keys<G, J>(l[U - 1])};
-    for (int r = 0; r < top; ++r) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            int first;
-            const uint32_t best = keys[u].take(first);
-            if (r == 0)
-                peak[u] = best;
-            const bool take = in == r && best != 0;
-            mine[u] = take ? best : mine[u];
-            id[u] = take ? first : id[u];
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const float top_logit = logit_of(peak[u]);
-        const float num = mine[u] ? expf(logit_of(mine[u]) - top_logit) : 0.0f;
-        float part = num;
-        if (!renorm) {
-            part = 0.0f;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                part += l[u][j] == -INFINITY ? 0.0f : expf(l[u][j] - top_logit);
-        }
-        const float total = group_sum<G>(part);
-        weight[u] = id[u] >= 0 ? num / total : 0.0f;
-    }
-}
-
-// Chooses for tokens [t0, t1), the workgroup's waves in turn, and calls
-// done(token, choice number, expert) from the lanes that hold them.
-template <int G, int J, typename F>
-__device__ __forceinline__ void choose_chunk(const void* logits, Act type, int64_t t0, int64_t t1, int e, int top,
-                                             bool renorm, float* weights, int32_t* experts, F&& done)
-{
-    constexpr int U = 2, T = U * kWave / G;  // tokens per wave
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, in = lane % G;
-    auto load = [&](int64_t t, float (&l)[U][J]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = t + u * (kWave / G) + lane / G;
-            load_logits<J>(logits, type, row < t1 ? row : t1 - 1, e, in * J, l[u]);
-        }
-    };
-    int64_t t = t0 + (int64_t)wave * T;
-    float next[U][J];
-    if (t < t1)
-        load(t, next);
-    for (; t < t1; t += kWaves * T) {
-        float l[U][J];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-                l[u][j] = next[u][j];
-        if (t + kWaves * T < t1)
-            load(t + kWaves * T, next);
-        float weight[U];
-        int id[U];
-        choose<G, J, U>(l, top, renorm, weight, id);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t row = t + u * (kWave / G) + lane / G;
-            if (in < top && row < t1) {
-                weights[row * top + in] = weight[u];
-                experts[row * top + in] = id[u];
-                done(row, in, id[u]);
-            }
-        }
-    }
-}
 
 // counts[c][i]: chunk c's slots of expert i, rows of `pitch`.
 template <int G, int J>
@@ -310,10 +49,12 @@ __global__ __launch_bounds__(kThreads) void route_choose_kernel(const void* __re
         hist[i] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * per, t1 = t0 + per < t ? t0 + per : t;
-    choose_chunk<G, J>(logits, type, t0, t1, e, top, renorm != 0, weights, experts, [&](int64_t, int, int id) {
-                           if (id >= 0)
-                               atomicAdd(&hist[id], 1);
-                       });
+    choose_chunk<G, J, kWaves>(logits, type, t0, t1, e, top, renorm != 0, [&](int64_t tok, int r, int id, float weight) {
+        weights[tok * top + r] = weight;
+        experts[tok * top + r] = id;
+        if (id >= 0)
+            atomicAdd(&hist[id], 1);
+    });
     __syncthreads();
     for (int i = threadIdx.x; i < pitch; i += kThreads)
         counts[(int64_t)blockIdx.x * pitch + i] = i < e ? hist[i] : 0;
@@ -499,11 +240,13 @@ __global__ __launch_bounds__(kThreads) void route_small_kernel(const void* __res
     total[i] = 0;
     clear_counts(p, e);
     __syncthreads();
-    choose_chunk<G, J>(logits, type, 0, t, e, top, renorm != 0, weights, experts, [&](int64_t tok, int r, int id) {
-                           chosen[tok * top + r] = (int16_t)id;
-                           if (id >= 0)
-                               atomicAdd(&total[id], 1);
-                       });
+    choose_chunk<G, J, kWaves>(logits, type, 0, t, e, top, renorm != 0, [&](int64_t tok, int r, int id, float weight) {
+        weights[tok * top + r] = weight;
+        experts[tok * top + r] = id;
+        chosen[tok * top + r] = (int16_t)id;
+        if (id >= 0)
+            atomicAdd(&total[id], 1);
+    });
     __syncthreads();
     const int mine = i < e ? total[i] : 0;
     const int incl = block_prefix(mine, p.waves);
@@ -536,19 +279,13 @@ int count_pitch(int64_t e)
     return (int)((e + 3) / 4 * 4);
 }
 
-// Lanes per token.
-int lanes(int64_t e, int64_t top)
-{
-    return e <= 64 && top <= 16 ? 16 : 64;
-}
-
 // One workgroup, one launch: one round of its waves, or few choices. The two
 // launches take 9 to 11 us however few the tokens; a round of one workgroup adds
 // about 0.35 us per choice (235 tokens, 6 of 44, in two rounds: 14.8 us against
 // 11.0; 250 tokens, 2 of 8: 7.4 against 9.3).
 bool small(int64_t t, int64_t e, int64_t top)
 {
-    const int64_t rounds = (t * lanes(e, top) + 2 * kThreads - 1) / (2 * kThreads);
+    const int64_t rounds = (t * choice_lanes(e, top) + 2 * kThreads - 1) / (2 * kThreads);
     return t * top <= kSmallSlots && (rounds <= 1 || rounds * (top + 2) <= 8);
 }
 
@@ -584,7 +321,7 @@ hipError_t launch_route(const void* logits, Act type, int64_t t, int64_t e, int6
 {
 #define FP8W_ROUTE(G, J)                                                                                               \
     return run<G, J>(logits, type, t, (int)e, (int)top, renorm, weights, experts, offsets, slots, tokens, ws, stream)
-    if (lanes(e, top) == 16) {
+    if (choice_lanes(e, top) == 16) {
         if (e <= 16)
             FP8W_ROUTE(16, 1);
         if (e <= 32)

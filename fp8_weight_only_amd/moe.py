@@ -21,6 +21,8 @@ CPU or PyTorch fallback.
     q, scale = quantize_fp4(w)                     # build time; w [n, k], or [e, n, k] for experts
     y = linear_fp4(x, q, scale, bias)
     h = linear_experts_fp4(x, qe, se, r.offsets, x_rows=r.tokens)
+
+    out = moe_layer(x, logits, top_k, (q, scale), (q2, scale2))    # all of a layer for up to 64 tokens
 """
 import contextlib
 import ctypes
@@ -56,13 +58,17 @@ MOE_EXPORTS = {
     "fp8w_linear_fp4_kernel": (ctypes.c_char_p, [_I64, _I64, _I64, _P, _P, _P]),
     "fp8w_linear_experts_fp4": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P]),
     "fp8w_linear_experts_fp4_kernel": (ctypes.c_char_p, [_I64, _I64, _I64, _I64, _P, _P, _P]),
+    "fp8w_moe_layer": (_I, [_P, _I, _I64, _I64, _P, _I, _I64, _I64, _I, _I, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _SZ,
+                            _P]),
+    "fp8w_moe_layer_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "fp8w_moe_last_hip_error": (_I, []),
 }
 
 __all__ = [*MOE_EXPORTS, "MOE_EXPORTS", "Fp8wMoeError", "moe_lib_path", "load_moe", "Route", "route",
            "quantize_experts", "linear_experts", "experts_workspace_bytes", "combine", "quantize_int8",
            "quantize_activations_int8", "gemm_int8", "linear_int8", "int8_workspace_bytes", "quantize_fp4",
-           "dequantize_fp4", "linear_fp4", "fp4_workspace_bytes", "linear_experts_fp4"]
+           "dequantize_fp4", "linear_fp4", "fp4_workspace_bytes", "linear_experts_fp4", "moe_layer",
+           "moe_layer_workspace_bytes", "MOE_LAYER_TOKENS", "WEIGHT_E4M3", "WEIGHT_FP4"]
 
 _LIB = None
 _FAST = None
@@ -190,6 +196,17 @@ def fp8w_linear_experts_fp4_kernel(m, e, n, k, x, q, scale):
     return r.decode() if r is not None else None
 
 
+def fp8w_moe_layer(x, act_dtype, t, hidden, logits, logits_dtype, e, top_k, renormalize, format, q_gate_up, scale_gate_up,
+                   bias_gate_up, inner, q_down, scale_down, bias_down, out, workspace, workspace_bytes, stream) -> int:
+    return load_moe().fp8w_moe_layer(x, act_dtype, t, hidden, logits, logits_dtype, e, top_k, renormalize, format,
+                                     q_gate_up, scale_gate_up, bias_gate_up, inner, q_down, scale_down, bias_down, out,
+                                     workspace, workspace_bytes, stream)
+
+
+def fp8w_moe_layer_workspace_bytes(t, e, top_k, hidden, inner) -> int:
+    return load_moe().fp8w_moe_layer_workspace_bytes(t, e, top_k, hidden, inner)
+
+
 def fp8w_moe_last_hip_error() -> int:
     return load_moe().fp8w_moe_last_hip_error()
 
@@ -203,6 +220,8 @@ _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _STATUS = ("success", "invalid value (size, dtype, NULL pointer or overlapping buffers)", "misaligned pointer",
            "non-finite weight (NaN or infinity)", "workspace missing or too small", "HIP runtime error")
 _ERR_HIP = 5
+MOE_LAYER_TOKENS = 64            # the most tokens that moe_layer takes
+WEIGHT_E4M3, WEIGHT_FP4 = 0, 1   # fp8w_weight_format_t
 
 
 class Fp8wMoeError(RuntimeError):
@@ -586,4 +605,63 @@ def linear_experts_fp4(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, of
     with _on(dev):
         st = fp8w_linear_experts_fp4(xp, act, rows, k, qp, sp, bp, e, n, op, m, ip, jp, yp, _stream(dev))
     _check(st, "fp8w_linear_experts_fp4")
+    return out
+
+
+def moe_layer_workspace_bytes(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up) -> int:
+    """The workspace of ``moe_layer`` on these, in bytes."""
+    t, e = logits.shape
+    return fp8w_moe_layer_workspace_bytes(t, e, top_k, x.shape[1], gate_up[0].shape[1] // 2)
+
+
+def moe_layer(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up, down, gate_up_bias: torch.Tensor = None,
+              down_bias: torch.Tensor = None, renormalize: bool = True, out: torch.Tensor = None,
+              workspace: torch.Tensor = None) -> torch.Tensor:
+    """A mixture-of-experts layer for up to 64 tokens, in two launches: ``route`` on the logits [t, e], each expert's
+    gate and up products on its tokens, silu(gate) * up, the down products, and the sum over a token's experts.
+
+    x: [t, hidden] bf16 / fp16. gate_up, down: (q, scale) pairs of weights [e, 2 inner, hidden] (gate's rows first)
+    and [e, hidden, inner], both from ``quantize_experts`` or both from ``quantize_fp4``. Biases [e, 2 inner] and
+    [e, hidden] of x.dtype. Sums in fp32; silu(gate) * up and the result are rounded to x.dtype. For more tokens call
+    ``route``, ``linear_experts`` (``linear_experts_fp4``) and ``combine``. ``workspace``: of
+    moe_layer_workspace_bytes, allocated when None."""
+    if workspace is None:
+        r = (_FAST or _fast()).moe_layer(x, logits, top_k, gate_up, down, gate_up_bias, down_bias, renormalize, out)
+        if r is not None:
+            return r if type(r) is not int else _check(r, "fp8w_moe_layer")
+    dev = _gpu(x, "x", 2)
+    _gpu(logits, "logits", 2)
+    t, hidden = x.shape
+    e = logits.shape[1]
+    (qu, su), (qd, sd) = gate_up, down
+    if qu.dim() != 3 or qd.dim() != 3 or qu.shape[1] % 2:
+        raise ValueError("gate_up and down must be (q, scale) of [e, 2 inner, hidden] and [e, hidden, inner] weights")
+    inner = qu.shape[1] // 2
+    if t > MOE_LAYER_TOKENS:
+        raise ValueError(f"moe_layer takes up to {MOE_LAYER_TOKENS} tokens, not {t}: call route, linear_experts "
+                         "(linear_experts_fp4) and combine")
+    if logits.dtype not in _DT:
+        raise TypeError(f"logits must be bf16, fp16 or fp32, not {logits.dtype}")
+    if not 1 <= top_k <= min(e, 64) or e > 1024:
+        raise ValueError("expected 1 <= top_k <= min(e, 64) and e <= 1024")
+    act = _act_code(x.dtype, "x")
+    fp4 = su.dtype is torch.uint8
+    xp = _want(x, "x", (t, hidden), x.dtype, dev)
+    lp = _want(logits, "logits", (t, e), logits.dtype, dev)
+    ptr = []
+    for name, q, s, n, k in (("gate_up", qu, su, 2 * inner, hidden), ("down", qd, sd, hidden, inner)):
+        ptr.append((_want(q, name + "[0]", (e, n, (k + 1) // 2 if fp4 else k), torch.uint8, dev),
+                    _want(s, name + "[1]", (e, n, (k + 31) // 32) if fp4 else (e, n),
+                          torch.uint8 if fp4 else torch.float32, dev)))
+    ub = _want(gate_up_bias, "gate_up_bias", (e, 2 * inner), x.dtype, dev)
+    db = _want(down_bias, "down_bias", (e, hidden), x.dtype, dev)
+    if out is None:
+        out = x.new_empty((t, hidden))
+    op = _want(out, "out", (t, hidden), x.dtype, dev)
+    workspace, wp, wb = _workspace(workspace, fp8w_moe_layer_workspace_bytes(t, e, top_k, hidden, inner), dev)
+    with _on(dev):
+        st = fp8w_moe_layer(xp, act, t, hidden, lp, _DT[logits.dtype], e, top_k, int(renormalize),
+                            WEIGHT_FP4 if fp4 else WEIGHT_E4M3, *ptr[0], ub, inner, *ptr[1], db, op, wp, wb,
+                            _stream(dev))
+    _check(st, "fp8w_moe_layer")
     return out

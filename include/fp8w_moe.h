@@ -202,6 +202,41 @@ FP8W_API fp8w_status_t fp8w_linear_experts_fp4(const void* x, fp8w_dtype_t act_d
 FP8W_API const char* fp8w_linear_experts_fp4_kernel(int64_t m, int64_t e, int64_t n, int64_t k, const void* x,
                                                     const uint8_t* q, const uint8_t* scale);
 
+/* Formats of a layer's weights. */
+typedef enum fp8w_weight_format {
+    FP8W_WEIGHT_E4M3 = 0, /* q [.., n, k] e4m3 codes, scale [.., n] fp32 */
+    FP8W_WEIGHT_FP4 = 1   /* q [.., n, (k + 1) / 2], scale [.., n, (k + 31) / 32] bytes */
+} fp8w_weight_format_t;
+
+/*
+ * A whole mixture-of-experts layer for a few tokens, in two launches:
+ *   choice and weights[t, j] of fp8w_route(logits, dtype, t, e, top_k, renormalize);
+ *   gate, up = the expert's rows 0 .. inner - 1 and inner .. 2 inner - 1 of q_gate_up
+ *              on x[t] (and their bias);
+ *   h        = gate / (1 + exp(-gate)) * up, rounded to act_dtype;
+ *   out[t]   = sum_j weights[t, j] * (the expert's q_down on h, and its bias),
+ * sums, scales, biases and the activation in fp32, out rounded once to act_dtype
+ * (BF16 or FP16). Places of the choice that are left over add nothing: a padding
+ * token's row is zeros. A token with a NaN weight has a row of NaN.
+ *   x, out     [t, hidden]; t <= 64 (more: fp8w_route, fp8w_linear_experts,
+ *              fp8w_combine). logits [t, e] of logits_dtype.
+ *   q_gate_up, scale_gate_up, bias_gate_up  [e, 2 inner, hidden] in `format`,
+ *              bias [e, 2 inner] of act_dtype or NULL.
+ *   q_down, scale_down, bias_down  [e, hidden, inner], [e, hidden].
+ *   hidden, inner >= 1, up to 2^22.
+ *   workspace of fp8w_moe_layer_workspace_bytes bytes, 16-byte aligned.
+ * out and workspace must not overlap an input or each other.
+ */
+FP8W_API fp8w_status_t fp8w_moe_layer(const void* x, fp8w_dtype_t act_dtype, int64_t t, int64_t hidden,
+                                      const void* logits, fp8w_dtype_t logits_dtype, int64_t e, int64_t top_k,
+                                      int renormalize, fp8w_weight_format_t format, const uint8_t* q_gate_up,
+                                      const void* scale_gate_up, const void* bias_gate_up, int64_t inner,
+                                      const uint8_t* q_down, const void* scale_down, const void* bias_down, void* out,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of fp8w_moe_layer; 0 for invalid sizes and for t == 0. */
+FP8W_API size_t fp8w_moe_layer_workspace_bytes(int64_t t, int64_t e, int64_t top_k, int64_t hidden, int64_t inner);
+
 /* The hipError_t behind this thread's last FP8W_ERR_HIP of this library. */
 FP8W_API int fp8w_moe_last_hip_error(void);
 
