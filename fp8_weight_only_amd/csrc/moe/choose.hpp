@@ -111,7 +111,7 @@ struct Keys {
     uint32_t key[J];
     uint32_t order;  // sorted: the registers' original numbers, a byte each, first key's lowest
 
-    __device__ __forceinline__ explicit Keys(const float (&l)[J])
+    __device__ __forceinline__ void set(const float (&l)[J])
     {
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -182,13 +182,12 @@ struct Keys {
     }
 };
 
-// Two tokens per group at a time (their chains of dependent steps overlap), from
+// U tokens per group at a time (two: their chains of dependent steps overlap), from
 // l[u][j], the token's logit of expert in * J + j. Lane r of a group gets its
 // tokens' r-th choice in id[u] (-1: none) and its weight.
 template <int G, int J, int U>
 __device__ __forceinline__ void choose(const float (&l)[U][J], int top, bool renorm, float (&weight)[U], int (&id)[U])
 {
-    static_assert(U == 2, "two tokens");
     const int in = (threadIdx.x & 63) % G;
     uint32_t mine[U], peak[U];
 #pragma unroll
@@ -196,7 +195,10 @@ __device__ __forceinline__ void choose(const float (&l)[U][J], int top, bool ren
         mine[u] = peak[u] = 0;
         id[u] = -1;
     }
-    Keys<G, J> keys[U] = {Keys<G, J>(l[0]), Keys<G, J>(l[U - 1])};
+    Keys<G, J> keys[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        keys[u].set(l[u]);
     for (int r = 0; r < top; ++r) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {

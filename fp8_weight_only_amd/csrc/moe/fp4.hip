@@ -10,7 +10,7 @@
 #include <stdio.h>
 
 #include "experts.hpp"
-#include "fp4.hpp"
+#include "stream.hpp"
 #include "tile.hpp"
 
 namespace fp8w {
@@ -32,149 +32,105 @@ __device__ __forceinline__ RowTile row_tile(const Fp4Call& c, int want)
 }
 
 // Few rows (decode): the weights stream once, straight into the matrix cores'
-// operand registers.
+// operand registers (stream.hpp).
 //
-// A workgroup owns 16 CT channels of up to 16 RT rows of one expert. Its W waves
-// split k in blocks of 256: a lane holds 32 codes, one scale's block, of channel
-// lane % 16 at k = 32 (lane / 16) of either half (one 16-byte load each), decodes
-// them, and feeds eight to each of four v_mfma_f32_16x16x32, the row's values at
-// the same k on the other side. A block's eight scales of a channel come in one
-// load. The next block's loads are in flight during a block's products. The waves'
-// sums meet in LDS and are added in wave order.
-//
-// Any k and any alignment: whole blocks take 16-byte loads from any dword (below
-// that, Row), the last k % 256 a masked step.
-template <typename A, int CT, int RT, int W, bool SHIFT>
-__global__ __launch_bounds__(W* kWave) void fp4_stream_kernel(Fp4Call c, int TN)
+// A workgroup has up to 16 rows of one expert and every cols-th tile of 16 CT WC
+// channels. Its waves are WC times WK: each owns 16 CT of a tile's channels and takes
+// every WK-th step of k; the sums of WK waves meet in LDS and are added in wave order.
+// A wave's loads run a step ahead, into the next tile's weights.
+template <typename A, int CT, int WK, int WC, Way WAY>
+__global__ __launch_bounds__(WK* WC* kWave) void fp4_stream_kernel(Fp4Call c, int TN, int cols)
 {
-    __shared__ __attribute__((aligned(16))) f32x4 part[W][CT * RT][kWave];
-    const int tn = blockIdx.x % TN;
-    const RowTile tile = row_tile<16 * RT>(c, blockIdx.x / TN);
+    using S = Stream<Fp4, A, CT, 1, 1, WAY, false>;
+    constexpr int W = WK * WC;
+    __shared__ __attribute__((aligned(16))) uint8_t ring[W][S::LDS];
+    __shared__ __attribute__((aligned(16))) f32x4 part[WK > 1 ? W : 1][CT][kWave];
+    const RowTile tile = row_tile<16>(c, blockIdx.x / cols);
     if (tile.expert < 0)
         return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)tn * (16 * CT);
-    f32x4 acc[CT][RT];
+    const int wk = wave % WK, wc = wave / WK, rows = uniform(tile.rows), expert = uniform(tile.expert);
+    const bool on = expert < (int)c.e;
+    // where this lane's row goes (-1: nowhere), and whether what it comes from exists
+    const int at = r < rows ? tile.row + r : tile.row;
+    int dst = c.y_rows ? c.y_rows[at] : at;
+    if (r >= rows || dst >= (int)c.m)
+        dst = -1;
+    const int64_t from = c.x_rows && on ? c.x_rows[at] : 0;
+    const bool ok = from >= 0 && (!c.x_rows || !on || from < c.xr);
+    // without a row list the rows are the tile's, from its first on
+    const int64_t first = c.x_rows ? 0 : uniform(tile.row);
+    S st(c.k, static_cast<const uint16_t*>(c.x) + first * c.k, on ? 2 * (c.xr - first) * c.k : 0, ring[wave]);
+    typename S::Source src;
+    st.rows(src, rows, [&](int i) { return (source_row(c, tile, i) - first) * c.k; });
+    auto enter = [&](int tn) {
+        const int64_t n0 = ((int64_t)tn * WC + wc) * (16 * CT);
+        st.weights(src, 0, c.q, c.block_scale, expert * c.n + n0, on ? c.e * c.n : 0);
+    };
+    const int NU = on ? (st.steps + WK - 1) / WK : 0;
+    int tn = blockIdx.x % cols;
+    enter(tn);
+    st.load(src, wk, wk < st.steps);
+#pragma unroll 1
+    for (; tn < TN; tn += cols) {
+        const int64_t n0 = ((int64_t)tn * WC + wc) * (16 * CT);
+        uint16_t bias[CT][4];
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
+        for (int t = 0; t < CT; ++t)
 #pragma unroll
-        for (int u = 0; u < RT; ++u)
-            acc[t][u] = f32x4{0.0f};
-    if (tile.expert < (int)c.e && c.xr > 0) {
-        Row<SHIFT> wp[CT], xp[RT];
-        const uint8_t* sp[CT];
+            for (int i = 0; i < 4; ++i) {
+                const int64_t ch = n0 + 16 * t + 4 * g + i;
+                bias[t][i] = bias_bits(static_cast<const uint16_t*>(c.bias), on && ch < c.n ? expert * c.n + ch : 0);
+            }
+        f32x4 acc[CT][1];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int64_t ch = n0 + 16 * t + r < c.n ? n0 + 16 * t + r : c.n - 1, row = (int64_t)tile.expert * c.n + ch;
-            wp[t] = Row<SHIFT>(c.q + row * c.row_bytes + 16 * g);
-            sp[t] = c.block_scale + row * c.row_scales;
+        for (int t = 0; t < CT; ++t)
+            acc[t][0] = f32x4{0.0f};
+#pragma unroll 1
+        for (int v = 0; v < NU; ++v) {
+            int ahead = v + 1;
+            bool more = true;
+            if (ahead == NU) {
+                ahead = 0;
+                more = tn + cols < TN;
+                if (more)
+                    enter(tn + cols);
+            }
+            ahead = wk + WK * ahead;
+            st.consume(wk + WK * v, src, ahead, more && ahead < st.steps, acc);
         }
+        // lane (r, g) holds channels 4 g .. 4 g + 3 of row r
+        auto store = [&](int t, f32x4 sum) {
+            const int64_t c0 = n0 + 16 * t + 4 * g;
+            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            uint16_t o[4];
 #pragma unroll
-        for (int u = 0; u < RT; ++u)
-            xp[u] = Row<SHIFT>(static_cast<const uint8_t*>(c.x) + 2 * (source_row(c, tile, 16 * u + r) * c.k + 32 * g));
-        struct Block {
-            typename Row<SHIFT>::Raw w[CT][2], x[RT][2][4];
-            u32x2 s[CT];
+            for (int i = 0; i < 4; ++i)
+                o[i] = on ? rounded<A>((ok ? v[i] : __builtin_nanf("")) + A::to_f32(bias[t][i])) : (uint16_t)0;
+            if (dst >= 0 && c0 < c.n)
+                store4(static_cast<uint16_t*>(c.y) + (int64_t)dst * c.n + c0, o, c.n - c0);
         };
-        auto load = [&](Block& b, int64_t kb) {
+        if constexpr (WK == 1) {
 #pragma unroll
             for (int t = 0; t < CT; ++t)
-                b.s[t] = *reinterpret_cast<const u32x2_any*>(sp[t] + kb / 32);
+                store(t, acc[t][0]);
+        } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int t = 0; t < CT; ++t)
+                part[wave][t][lane] = acc[t][0];
+            lds_barrier();
 #pragma unroll
-                for (int t = 0; t < CT; ++t)
-                    b.w[t][h] = wp[t].load(kb / 2 + 64 * h);
+            for (int t = 0; t < CT; ++t)
+                if (t % WK == wk) {
+                    f32x4 sum = part[wc * WK][t][lane];
 #pragma unroll
-                for (int u = 0; u < RT; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        b.x[u][h][j] = xp[u].load(2 * kb + 256 * h + 16 * j);
-            }
-        };
-        auto products = [&](const u32x4 (&w)[CT], const float (&s)[CT], const u32x4 (&x)[RT][4]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    const u32x4 v = w[t];
-                    const u32x4 a = decode_fp4<A>(j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w)), s[t]);
-#pragma unroll
-                    for (int u = 0; u < RT; ++u)
-                        acc[t][u] = A::mfma(a, x[u][j], acc[t][u]);
+                    for (int w = 1; w < WK; ++w)
+                        sum += part[wc * WK + w][t][lane];
+                    store(t, sum);
                 }
-        };
-        auto compute = [&](const Block& b) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 w[CT], x[RT][4];
-                float s[CT];
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    w[t] = wp[t].bytes(b.w[t][h]);
-                    const u32x2 s8 = b.s[t];
-                    s[t] = fp4_scale(((h ? s8.y : s8.x) >> (8 * g)) & 255u);
-                }
-#pragma unroll
-                for (int u = 0; u < RT; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[u][j] = xp[u].bytes(b.x[u][h][j]);
-                products(w, s, x);
-            }
-        };
-        // this wave's blocks: wave, wave + W, .. below k / 256
-        const int64_t whole = c.k / 256;
-        int64_t b = wave;
-        if (b < whole) {
-            Block cur;
-            load(cur, 256 * b);
-            for (b += W; b < whole; b += W) {
-                Block next;
-                load(next, 256 * b);
-                compute(cur);
-                cur = next;
-            }
-            compute(cur);
+            if (tn + cols < TN)
+                lds_barrier();
         }
-        const int64_t kb = 256 * whole;
-        if (kb < c.k && wave == (int)(whole % W)) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int64_t left = c.k - kb - 128 * h - 32 * g;  // weights from this lane's first on
-                u32x4 w[CT], x[RT][4];
-                float s[CT];
-#pragma unroll
-                for (int t = 0; t < CT; ++t) {
-                    w[t] = first_codes(wp[t].part(kb / 2 + 64 * h, (left + 1) / 2), left);
-                    s[t] = fp4_scale(left > 0 ? sp[t][kb / 32 + 4 * h + g] : 127);
-                }
-#pragma unroll
-                for (int u = 0; u < RT; ++u)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[u][j] = xp[u].part(2 * kb + 256 * h + 16 * j, 2 * left - 16 * j);
-                products(w, s, x);
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-        for (int u = 0; u < RT; ++u)
-            part[wave][t * RT + u][lane] = acc[t][u];
-    __syncthreads();
-    // lane (r, g) holds channels 4 g .. 4 g + 3 of row r
-    for (int t = wave; t < CT * RT; t += W) {
-        f32x4 sum = part[0][t][lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w)
-            sum += part[w][t][lane];
-        const int64_t c0 = n0 + 16 * (t / RT) + 4 * g, left = c.n - c0;
-        const int row = 16 * (t % RT) + r;
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-        if (row < tile.rows && left > 0)
-            store_tile_row<A, false>(c, tile.row + row, tile.expert, c0, left < 4 ? (int)left : 4, v);
     }
 }
 
@@ -185,10 +141,10 @@ __global__ __launch_bounds__(W* kWave) void fp4_stream_kernel(Fp4Call c, int TN)
 // bytes per row then meets each bank twice, without it four times. Eight bytes are
 // 16 codes, for two v_mfma_f32_32x32x16 of eight k each; both lie in one scale's
 // block (a half of a stage is 32 k).
-template <typename A, int BN, int BM, int WN, int WM>
+template <typename A, int BN, int BM, int WN, int WM, int Q = 1>
 struct Fp4Tile {
     static constexpr int W = WN * WM, NT = W * kWave, FN = BN / WN / 32, FM = BM / WM / 32;
-    static constexpr int ABYTES = BN * 32, STAGE = ABYTES + BM * 128;
+    static constexpr int ABYTES = BN * 32 * Q, XBYTES = BM * 128, STAGE = ABYTES + XBYTES * Q;
     static_assert(BN == FN * WN * 32 && BM == FM * WM * 32, "tile and wave layout");
     struct Frags {
         u32x2 a[FN];
@@ -197,16 +153,19 @@ struct Fp4Tile {
     };
     int lane, wave, wn, wm;
 
-    // everything but the scales
+    // where a row's 16-byte chunk of codes lies in its 2 Q: 256 bytes of chunks of one number hold 16 rows'
+    __device__ __forceinline__ static int place(int r, int chunk) { return (chunk ^ (r / (8 / Q))) & (2 * Q - 1); }
+
+    // everything but the scales, of 32 k: part j of the stage's 2 Q
     __device__ __forceinline__ void read_operands(const uint8_t* buf, int j, Frags& f) const
     {
-        const int i = lane & 31, h = lane >> 5;
-        const int oa = 32 * (wn * (BN / WN) + i) + 16 * ((j + (i >> 3)) & 1) + 8 * h;
-        const int ox = ABYTES + 128 * (wm * (BM / WM) + i);
-        const int o0 = ox + 16 * ((4 * j + 2 * h + (i >> 1)) & 7), o1 = ox + 16 * ((4 * j + 2 * h + 1 + (i >> 1)) & 7);
+        const int i = lane & 31, h = lane >> 5, t = 4 * (j & 1) + 2 * h + (i >> 1);
+        const int oa = 32 * Q * (wn * (BN / WN) + i) + 16 * place(i, j) + 8 * h;
+        const int ox = ABYTES + XBYTES * (j / 2) + 128 * (wm * (BM / WM) + i);
+        const int o0 = ox + 16 * (t & 7), o1 = ox + 16 * ((t + 1) & 7);
 #pragma unroll
         for (int q = 0; q < FN; ++q)
-            f.a[q] = *reinterpret_cast<const u32x2*>(buf + (oa + 1024 * q));
+            f.a[q] = *reinterpret_cast<const u32x2*>(buf + (oa + 1024 * Q * q));
 #pragma unroll
         for (int q = 0; q < FM; ++q)
             f.x[q][0] = *reinterpret_cast<const u32x4*>(buf + (o0 + 4096 * q));
@@ -236,13 +195,13 @@ struct Fp4Tile {
 
 // Which tile this workgroup is (false: none).
 template <int BM>
-__device__ __forceinline__ bool find_fp4_tile(const Fp4Call& c, int TN, int& tn, RowTile& tile)
+__device__ __forceinline__ bool find_fp4_tile(const Fp4Call& c, int TN, int block, int& tn, RowTile& tile)
 {
     if (c.offsets)
         return find_tile<BM>(c, TN, tn, tile);
     int tm;
     const int TM = (int)((c.m + BM - 1) / BM);
-    xcd_tile<4>(blockIdx.x, TN, TM, tn, tm);
+    xcd_tile<4>(block, TN, TM, tn, tm);
     const int left = (int)c.m - tm * BM;
     tile = RowTile{0, tm * BM, left < BM ? left : BM};
     return true;
@@ -262,7 +221,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_tile_kernel(Fp4Call c, int 
     __shared__ __attribute__((aligned(16))) ExpertEpilogue<BN, BM> epi;
     int tn;
     RowTile tile;
-    if (!find_fp4_tile<BM>(c, TN, tn, tile))
+    if (!find_fp4_tile<BM>(c, TN, blockIdx.x, tn, tile))
         return;
     const int64_t n0 = (int64_t)tn * BN;
     const int tid = threadIdx.x;
@@ -356,60 +315,70 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_tile_kernel(Fp4Call c, int 
     store_tile<A, BN, BM, WN, WM>(c, p, n0, epi, acc);
 }
 
-// Rows at 16-byte boundaries, k a multiple of 128, scales at dword boundaries, x
-// below 2 GiB: the same tiles fed by a ring of NS direct-to-LDS stages (tile.hpp).
-// A stage brings each channel's four scales of 128 k, of which it uses two: the
-// lower pair in an even stage, the upper in an odd one.
+// Rows at 16-byte boundaries, k a multiple of 64 Q (and of 128), scales at dword
+// boundaries, x below 2 GiB: the same tiles fed by a ring of NS direct-to-LDS stages
+// (tile.hpp) of 64 Q k. Scales come as dwords of 128 k: a stage of 64 k uses half of
+// it, the lower pair in an even stage, the upper in an odd one.
 template <int I>
 struct RingSlot {
     static constexpr int index = I;
     uint8_t* p;
 };
 
-template <typename A, int BN, int BM, int WN, int WM, int NS>
-struct Fp4Ring : Fp4Tile<A, BN, BM, WN, WM> {
-    using T = Fp4Tile<A, BN, BM, WN, WM>;
+template <typename A, int BN, int BM, int WN, int WM, int NS, int Q>
+struct Fp4Ring : Fp4Tile<A, BN, BM, WN, WM, Q> {
+    using T = Fp4Tile<A, BN, BM, WN, WM, Q>;
     using Frags = typename T::Frags;
-    static constexpr int STAGE = T::STAGE + BN * 4;
+    static constexpr int SD = Q > 1 ? Q / 2 : 1;  // dwords of a channel's scales
+    static constexpr int STAGE = T::STAGE + BN * 4 * SD;
     // 1 KB pieces of a stage's codes, 256-byte pieces of its scales; where there are fewer than waves, some load the same
-    static constexpr int KW = BN / 32, KS = BN / 64;
-    static constexpr int LW = KW > T::W ? KW / T::W : 1, LX = BM / 8 / T::W, LOADS = LW + LX + 1;
+    static constexpr int KW = BN * Q / 32, KS = BN * SD / 64;
+    static constexpr int LW = KW > T::W ? KW / T::W : 1, LX = BM * Q / 8 / T::W, LS = KS > T::W ? KS / T::W : 1;
+    static constexpr int LOADS = LW + LX + LS;
     static_assert(KW % T::W == 0 || T::W % KW == 0, "code pieces split evenly, or waves load the same");
-    static_assert(BM == LX * 8 * T::W && KS >= 1 && KS <= T::W, "loads split evenly");
+    static_assert(KS % T::W == 0 || T::W % KS == 0, "scale pieces split evenly, or waves load the same");
+    static_assert(BM * Q == LX * 8 * T::W && KS >= 1, "loads split evenly");
     Rows w, x, sc;
     int off[LOADS];  // this lane's part of each load at k = 0
-    int S, rot;
+    int S, rot, s0;  // stages, the one to begin with, the slice's first
     mutable int upper[NS];  // the bit in its dword where a stage's pair of scales starts
 
     template <int I>
     __device__ __forceinline__ void issue(int s, RingSlot<I> slot) const
     {
-        const int st = s + rot < S ? s + rot : s + rot - S, kb = 64 * st;
-        upper[I] = 16 * (st & 1);
+        const int st = s0 + (s + rot < S ? s + rot : s + rot - S), kb = 64 * Q * st;
+        upper[I] = Q == 1 ? 16 * (st & 1) : 0;
 #pragma unroll
         for (int u = 0; u < LW; ++u)
             w.load(off[u], kb / 2, slot.p + 1024 * ((u * T::W + this->wave) % KW));
 #pragma unroll
         for (int u = 0; u < LX; ++u)
             x.load(off[LW + u], 2 * kb, slot.p + T::ABYTES + 1024 * (u * T::W + this->wave));
-        sc.load4(off[LW + LX], 4 * (st / 2), slot.p + T::STAGE + 256 * (this->wave % KS));
+#pragma unroll
+        for (int u = 0; u < LS; ++u)
+            sc.load4(off[LW + LX + u], kb / 128 * 4, slot.p + T::STAGE + 256 * ((u * T::W + this->wave) % KS));
     }
 
     template <int I>
     __device__ __forceinline__ void read(RingSlot<I> slot, int j, Frags& f) const
     {
         this->read_operands(slot.p, j, f);
-        const int os = T::STAGE + 4 * (this->wn * (BN / WN) + (this->lane & 31));
+        const int os = T::STAGE + 4 * SD * (this->wn * (BN / WN) + (this->lane & 31));
 #pragma unroll
-        for (int q = 0; q < T::FN; ++q)
-            f.s[q] = fp4_scale((*reinterpret_cast<const uint32_t*>(slot.p + (os + 128 * q)) >> (upper[I] + 8 * j)) & 255u);
+        for (int q = 0; q < T::FN; ++q) {
+            const uint8_t* at = slot.p + (os + 128 * SD * q);
+            if constexpr (Q == 1)
+                f.s[q] = fp4_scale((*reinterpret_cast<const uint32_t*>(at) >> (upper[I] + 8 * j)) & 255u);
+            else
+                f.s[q] = fp4_scale(at[j]);
+        }
     }
 };
 
 // A wave whose rows all lie past the tile's: it loads its share and keeps the
 // barriers, and leaves the matrix cores to the others.
-template <typename A, int BN, int BM, int WN, int WM, int NS>
-struct Fp4RingIdle : Fp4Ring<A, BN, BM, WN, WM, NS> {
+template <typename A, int BN, int BM, int WN, int WM, int NS, int Q>
+struct Fp4RingIdle : Fp4Ring<A, BN, BM, WN, WM, NS, Q> {
     struct Frags {};
     template <int I>
     __device__ __forceinline__ void read(RingSlot<I>, int, Frags&) const
@@ -418,24 +387,78 @@ struct Fp4RingIdle : Fp4Ring<A, BN, BM, WN, WM, NS> {
     __device__ __forceinline__ void mma(const Frags&, f32x16*) const {}
 };
 
-template <typename A, int BN, int BM, int WN, int WM, int NS>
-__global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int TN)
+// A k split's sums: parts[slice, row, channel], rows of whole fours.
+constexpr int kJoinThreads = 256;
+__host__ __device__ constexpr int64_t parts_row(int64_t n) { return (n + 3) / 4 * 4; }
+
+template <int BN, int BM, int WN, int WM, typename P>
+__device__ __forceinline__ void store_sums(const Fp4Call& c, const P& p, float* part, const RowTile& tile, int64_t n0,
+                                           const f32x16* acc)
 {
-    using P = Fp4Ring<A, BN, BM, WN, WM, NS>;
-    using T = Fp4Tile<A, BN, BM, WN, WM>;
-    static_assert(NS >= 3 && NS <= 4, "stages");
+    const int i = p.lane & 31, h = p.lane >> 5;
+#pragma unroll
+    for (int fm = 0; fm < P::FM; ++fm) {
+        const int row = p.wm * (BM / WM) + 32 * fm + i;
+        if (row >= tile.rows)
+            continue;
+#pragma unroll
+        for (int fn = 0; fn < P::FN; ++fn)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t c0 = n0 + p.wn * (BN / WN) + 32 * fn + 8 * j + 4 * h;
+                const f32x16& a = acc[fn * P::FM + fm];
+                if (c0 < c.n)
+                    *reinterpret_cast<f32x4*>(part + (tile.row + row) * parts_row(c.n) + c0) =
+                        f32x4{a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]};
+            }
+    }
+}
+
+// Adds the slices of a k split in their order: four channels of a row a thread.
+template <typename A>
+__global__ __launch_bounds__(kJoinThreads) void fp4_join_kernel(Fp4Call c, int slices)
+{
+    const int64_t row4 = parts_row(c.n), item = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+    const int64_t row = 4 * item / row4, c0 = 4 * item - row * row4;
+    if (row >= c.m)
+        return;
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int z = 0; z < slices; ++z)
+        sum += *reinterpret_cast<const f32x4*>(c.parts + (z * c.m + row) * row4 + c0);
+    uint16_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        o[e] = rounded<A>(sum[e] + A::to_f32(bias_bits(static_cast<const uint16_t*>(c.bias), c0 + e < c.n ? c0 + e : 0)));
+    store4(static_cast<uint16_t*>(c.y) + row * c.n + c0, o, c.n - c0);
+}
+
+template <typename A, int BN, int BM, int WN, int WM, int NS, int Q>
+__global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int TN, int tiles, int slices)
+{
+    using P = Fp4Ring<A, BN, BM, WN, WM, NS, Q>;
+    using T = Fp4Tile<A, BN, BM, WN, WM, Q>;
+    static_assert(NS >= 2 && NS <= 8, "stages");
     __shared__ __attribute__((aligned(1024))) uint8_t b0[P::STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t b1[P::STAGE];
-    __shared__ __attribute__((aligned(1024))) uint8_t b2[P::STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t b2[NS > 2 ? P::STAGE : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t b3[NS > 3 ? P::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b4[NS > 4 ? P::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b5[NS > 5 ? P::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b6[NS > 6 ? P::STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t b7[NS > 7 ? P::STAGE : 16];
     __shared__ __attribute__((aligned(16))) ExpertEpilogue<BN, BM> epi;
     auto buf = [&](auto ic) {
         constexpr int i = decltype(ic)::value;
-        return RingSlot<i>{ring_buf<i>(b0, b1, b2, b3)};
+        if constexpr (i < 4)
+            return RingSlot<i>{ring_buf<i>(b0, b1, b2, b3)};
+        else
+            return RingSlot<i>{ring_buf<i - 4>(b4, b5, b6, b7)};
     };
     int tn;
     RowTile tile;
-    if (!find_fp4_tile<BM>(c, TN, tn, tile))
+    const int slice = slices > 1 ? (int)blockIdx.x / tiles : 0;
+    if (!find_fp4_tile<BM>(c, TN, (int)blockIdx.x - slice * tiles, tn, tile))
         return;
     const int64_t n0 = (int64_t)tn * BN;
     const int tid = threadIdx.x;
@@ -450,7 +473,9 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
         acc[f] = f32x16{0.0f};
     fill_epilogue<BN, BM, T::NT, false>(c, tile, n0, epi);
     if (tile.expert < (int)c.e && c.xr > 0) {
-        p.S = (int)(c.k / 64);
+        const int S = (int)(c.k / (64 * Q));
+        p.s0 = slice * S / slices;
+        p.S = (slice + 1) * S / slices - p.s0;
         p.rot = (int)(blockIdx.x % 8) * (p.S / 8);
         const int64_t first = (int64_t)tile.expert * c.n + n0;
         p.w = Rows(c.q + first * c.row_bytes);
@@ -459,22 +484,32 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
         auto row = [&](int r) { return (int)(n0 + r < c.n ? r : c.n - 1 - n0); };
 #pragma unroll
         for (int u = 0; u < P::LW; ++u) {
-            const int r = 32 * ((u * T::W + p.wave) % P::KW) + (p.lane >> 1);
-            p.off[u] = row(r) * (int)c.row_bytes + 16 * (((p.lane & 1) - (r >> 3)) & 1);
+            const int r = 32 / Q * ((u * T::W + p.wave) % P::KW) + p.lane / (2 * Q);
+            p.off[u] = row(r) * (int)c.row_bytes + 16 * T::place(r, p.lane % (2 * Q));
         }
 #pragma unroll
         for (int u = 0; u < P::LX; ++u) {
-            const int r = 8 * (u * T::W + p.wave) + (p.lane >> 3);
-            p.off[P::LW + u] = (int)(2 * source_row(c, tile, r) * c.k) + 16 * (((p.lane & 7) - (r >> 1)) & 7);
+            const int piece = u * T::W + p.wave, r = 8 * (piece % (BM / 8)) + (p.lane >> 3);
+            p.off[P::LW + u] = (int)(2 * source_row(c, tile, r) * c.k) + 128 * (piece / (BM / 8)) +
+                               16 * (((p.lane & 7) - (r >> 1)) & 7);
         }
-        p.off[P::LW + P::LX] = row(64 * (p.wave % P::KS) + p.lane) * (int)c.row_scales;
+#pragma unroll
+        for (int u = 0; u < P::LS; ++u) {
+            const int at = 64 * ((u * T::W + p.wave) % P::KS) + p.lane;
+            p.off[P::LW + P::LX + u] = row(at / P::SD) * (int)c.row_scales + 4 * (at % P::SD);
+        }
         if (p.wm * (BM / WM) < tile.rows) {
-            run_tile_ring<NS, P::LOADS>(p, p.S, buf, acc);
+            run_tile_ring<NS, P::LOADS, 2 * Q>(p, p.S, buf, acc);
         } else {
-            Fp4RingIdle<A, BN, BM, WN, WM, NS> idle;
+            Fp4RingIdle<A, BN, BM, WN, WM, NS, Q> idle;
             static_cast<P&>(idle) = p;
-            run_tile_ring<NS, P::LOADS>(idle, p.S, buf, acc);
+            run_tile_ring<NS, P::LOADS, 2 * Q>(idle, p.S, buf, acc);
         }
+    }
+    __syncthreads();
+    if (slices > 1) {
+        store_sums<BN, BM, WN, WM>(c, p, c.parts + slice * c.m * parts_row(c.n), tile, n0, acc);
+        return;
     }
     __syncthreads();
     store_tile<A, BN, BM, WN, WM>(c, p, n0, epi, acc);
@@ -597,71 +632,116 @@ unsigned capped_grid(int64_t threads)
 // ------------------------------------------------------------------ plans
 enum class Fp4Kind { STREAM, TILE, RING };
 
+// A kernel's tile, and what its calls take: start us, and for every 64 k of a
+// workgroup's k, wait and for every workgroup on its CU each + rows_part (of 16 rows in use;
+// less of fewer) us. Fitted to sweeps over layers of [1024, 1024] to [28672, 8192] with 1 to
+// 4096 rows (a stream's own three: one row, [28672, 8192], {2, 1, 4} 29.7, {2, 2, 2} 30.6, {1, 4, 1}
+// 36.8; [14336, 4096]: 15.0, 10.8, 13.4; [8192, 4096]: 14.3, 9.6, 8.4). The plan with the lowest
+// modelled time was the fastest measured or within 3 % of it in 40 of 44 calls, 15 % off at worst.
 struct Fp4Plan {
     Fp4Kind kind;
-    int a, b, w;  // stream: CT, RT, W; tile, ring: BN, BM, waves
-    int64_t channels() const { return kind == Fp4Kind::STREAM ? 16 * a : a; }
-    int64_t rows() const { return kind == Fp4Kind::STREAM ? 16 * b : b; }
-    bool fits(const Fp4Shape& s) const { return grid_fits(groups(s), w * kWave); }
-    int64_t groups(const Fp4Shape& s) const { return (s.n + channels() - 1) / channels() * s.row_tiles(rows()); }
+    int a, b, w;  // stream: CT, 16, WK; tile, ring: BN, BM, waves
+    int c;        // stream: WC
+    double start, wait, each, rows_part;
+    int slices = 1;  // ring: parts of k
+    int64_t channels() const { return kind == Fp4Kind::STREAM ? 16 * a * c : a; }
+    int64_t groups(const Fp4Shape& s) const { return (s.n + channels() - 1) / channels() * s.row_tiles(b) * slices; }
+    bool fits(const Fp4Shape& s) const { return grid_fits(groups(s), w * c * kWave); }
+    // active experts of rows rows each
+    double us(const Fp4Shape& s, int64_t active, int64_t rows) const
+    {
+        const int64_t tiles = (s.n + channels() - 1) / channels() * active * ((rows + b - 1) / b);
+        const double share = (double)(rows < 16 ? rows : 16) / 16.0;
+        double t = start + (double)s.k / (64.0 * slices) *
+                               (wait + (double)((tiles * slices + 255) / 256) * (each + rows_part * share));
+        if (slices > 1)  // the join's launch, the sums it reads
+            t += 3.0 + 2.9e-6 * (double)slices * (double)s.m * (double)s.n;
+        return t;
+    }
 };
 
-constexpr Fp4Plan kRings[] = {{Fp4Kind::RING, 256, 256, 8}, {Fp4Kind::RING, 256, 128, 8}, {Fp4Kind::RING, 128, 128, 8},
-                              {Fp4Kind::RING, 256, 64, 8},  {Fp4Kind::RING, 128, 64, 4},  {Fp4Kind::RING, 64, 64, 4},
-                              {Fp4Kind::RING, 256, 32, 4},  {Fp4Kind::RING, 128, 32, 4},  {Fp4Kind::RING, 64, 32, 2}};
-constexpr Fp4Plan kTiles[] = {{Fp4Kind::TILE, 256, 128, 8},
-                              {Fp4Kind::TILE, 128, 64, 4},
-                              {Fp4Kind::TILE, 64, 64, 4},
-                              {Fp4Kind::TILE, 128, 32, 4}};
+constexpr Fp4Plan kStreams[] = {{Fp4Kind::STREAM, 1, 16, 4, 1, 3.0, 0.0, 0.035, 0.035},
+                                {Fp4Kind::STREAM, 2, 16, 2, 2, 3.0, 0.0, 0.086, 0.058},
+                                {Fp4Kind::STREAM, 2, 16, 1, 4, 3.0, 0.0, 0.17, 0.11}};
+constexpr Fp4Plan kRings[] = {
+    {Fp4Kind::RING, 64, 32, 2, 1, 3.8, 0.05, 0.099, 0.0},  {Fp4Kind::RING, 128, 32, 4, 1, 3.8, 0.0, 0.191, 0.0},
+    {Fp4Kind::RING, 64, 64, 4, 1, 3.8, 0.0, 0.198, 0.0},   {Fp4Kind::RING, 128, 64, 4, 1, 3.8, 0.0, 0.36, 0.0},
+    {Fp4Kind::RING, 128, 128, 8, 1, 3.8, 0.0, 0.70, 0.0},  {Fp4Kind::RING, 256, 128, 8, 1, 3.8, 0.0, 1.13, 0.0},
+    {Fp4Kind::RING, 256, 256, 8, 1, 3.8, 0.0, 1.78, 0.0}};
+constexpr Fp4Plan kTiles[] = {{Fp4Kind::TILE, 256, 128, 8, 1, 0.0, 0.0, 0.0, 0.0},
+                              {Fp4Kind::TILE, 128, 64, 4, 1, 0.0, 0.0, 0.0, 0.0},
+                              {Fp4Kind::TILE, 64, 64, 4, 1, 0.0, 0.0, 0.0, 0.0},
+                              {Fp4Kind::TILE, 128, 32, 4, 1, 0.0, 0.0, 0.0, 0.0}};
+
+// Where LDS has room, a stage is 256 k: whole 128-byte lines of codes. With stages of 64 k
+// each line is fetched four times, and [4096, 14336] with 22 rows takes 20.0 us instead of 15.1,
+// [14336, 4096] with 64 rows 24.4 instead of 17.8.
+constexpr int ring_units(int bm)
+{
+    return bm <= 64 ? 4 : 1;
+}
 
 constexpr int ring_depth(int bn, int bm)
 {
-    return bn == 256 && bm == 256 ? 3 : 4;
+    return bm <= 64 || bn * bm == 65536 ? 3 : 4;
 }
 
-Fp4Plan stream_plan(const Fp4Shape& s, int64_t active, int64_t rows)
+// Workgroups on a row tile's channels: all of the channel tiles while there are few, else
+// each goes on to the next tile with loads in flight (512 rows above: 70 us a workgroup
+// a tile, 65 with 1024 workgroups, 62 with 2048).
+int64_t stream_columns(int64_t tiles, int64_t TN)
 {
-    const int rt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-    Fp4Plan p{Fp4Kind::STREAM, rt == 1 ? 4 : (rt == 2 ? 2 : 1), rt, s.k >= 2048 ? 8 : 4};
-    while (p.a > 1 && (s.n + 16 * p.a - 1) / (16 * p.a) * active < 256)
-        p.a /= 2;
-    return p;
+    const int64_t most = (2048 + tiles - 1) / tiles;
+    return TN < most ? TN : most;
 }
 
+// Offsets of an int.
+bool stream_fits(const Fp4Shape& s, const Fp4Plan& p)
+{
+    const int64_t rows = s.grouped ? s.xr : 16;
+    return p.fits(s) && s.k <= (1 << 22) && rows * s.k < (1 << 29);
+}
+
+// aligned: rows and scales as the ring and the stream's LDS way take them.
 Fp4Plan fp4_plan(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale)
 {
-    const int64_t active = !s.grouped ? 1 : (s.m < s.e ? s.m : s.e), rows = (s.m + active - 1) / active;
+    const int64_t most = s.m < s.e ? s.m : s.e, active = s.grouped && most > 0 ? most : 1, rows = (s.m + active - 1) / active;
     const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q)) & 15) == 0 &&
-                         (reinterpret_cast<uintptr_t>(scale) & 3) == 0;
-    const bool ring =
-        aligned && s.k % 128 == 0 && s.k >= 320 && s.k <= (1 << 22) && s.xr <= ((int64_t)1 << 30) / s.k;
-    const Fp4Plan st = stream_plan(s, active, rows);
-    const bool streams = st.fits(s);
-    if (rows <= 16 && streams)
-        return st;
-    auto fills = [&](const Fp4Plan& p, int64_t least) {
-        return (s.n + p.a - 1) / p.a * active * ((rows + p.b - 1) / p.b) >= least && p.fits(s);
-    };
-    if (ring) {
-        const int bm = rows <= 16 ? 32 : (rows <= 48 ? 64 : (rows <= 192 ? 128 : 256));
-        for (const Fp4Plan& p : kRings) {
-            if (p.b > bm || (p.a == 256 && p.b == 32 && s.k < 2048))
-                continue;
-            if (fills(p, p.b == 256 ? 128 : 224))
-                return p;
+                         (reinterpret_cast<uintptr_t>(scale) & 3) == 0 && s.k % 128 == 0;
+    Fp4Plan found{};
+    double low = 0.0;
+    bool any = false;
+    auto offer = [&](const Fp4Plan& p) {
+        const double us = p.us(s, active, rows);
+        if (!any || us < low) {
+            found = p;
+            any = true;
+            low = us;
         }
-    } else {
-        const int bm = rows <= 16 ? 32 : (rows <= 96 ? 64 : 128);
-        for (const Fp4Plan& p : kTiles)
-            if (p.b <= bm && fills(p, 224))
-                return p;
+    };
+    for (const Fp4Plan& p : kStreams)
+        if ((rows <= 16 || aligned) && stream_fits(s, p))
+            offer(p);
+    // Few rows to an expert: rings of 32 rows load and multiply mostly nothing (128 experts of
+    // [4096, 1024], four rows each: 91 us, the stream 62).
+    const bool few = s.grouped && rows <= 16 && any;
+    if (aligned && !few && s.k > 0 && s.k <= (1 << 22) && s.xr <= ((int64_t)1 << 30) / s.k) {
+        for (const Fp4Plan& p : kRings)
+            for (int z = 1; z <= (s.grouped ? 1 : 16); z *= 2) {
+                Fp4Plan v = p;
+                v.slices = z;
+                const int64_t stage = 64 * ring_units(p.b);
+                if (s.k % stage == 0 && s.k / stage / z >= ring_depth(p.a, p.b) && v.fits(s))
+                    offer(v);
+            }
     }
-    if (rows <= 64 && streams)
-        return st;
-    for (const Fp4Plan& p : kRings)
-        if (ring && p.a == 64 && p.b == 64 && p.fits(s))
+    if (any)
+        return found;
+    const int bm = rows <= 16 ? 32 : (rows <= 96 ? 64 : 128);
+    for (const Fp4Plan& p : kTiles)
+        if (p.b <= bm && (s.n + p.a - 1) / p.a * active * ((rows + p.b - 1) / p.b) >= 224 && p.fits(s))
             return p;
-    return {Fp4Kind::TILE, 64, 64, 4};
+    return kTiles[2];
 }
 
 Fp4Shape shape_of(const Fp4Call& c)
@@ -677,12 +757,29 @@ bool shifted(const Fp4Call& c)
             3) != 0;
 }
 
-template <typename A, int CT, int RT, int W>
+// LDS takes rows at 16-byte boundaries, and scales at dwords, in steps of four units: where
+// those are fewer than the waves they are for, the shorter steps keep more of them busy
+// (one row, [1024, 1024]: 3.6 us against 5.0; of [1024, 2048] it is 4.3 against 3.9).
+Way stream_way(const Fp4Call& c, int wk)
+{
+    if (shifted(c))
+        return Way::SHIFTED;
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(c.x) | reinterpret_cast<uintptr_t>(c.q) | (uintptr_t)(2 * c.k) |
+                           (uintptr_t)c.row_bytes;
+    const uintptr_t scales = reinterpret_cast<uintptr_t>(c.block_scale) | (uintptr_t)c.row_scales;
+    return (rows & 15) == 0 && (scales & 3) == 0 && c.k > 4 * Fp4::kUnit * (wk - 1) ? Way::LDS : Way::ROWS;
+}
+
+template <typename A, int CT, int WK, int WC>
 hipError_t run_stream(const Fp4Call& c, hipStream_t stream)
 {
-    const int64_t TN = (c.n + 16 * CT - 1) / (16 * CT), groups = TN * shape_of(c).row_tiles(16 * RT);
-    return launch(shifted(c) ? fp4_stream_kernel<A, CT, RT, W, true> : fp4_stream_kernel<A, CT, RT, W, false>,
-                  dim3((unsigned)groups), dim3(W * kWave), stream, c, TN);
+    const int64_t TN = (c.n + 16 * CT * WC - 1) / (16 * CT * WC), tiles = shape_of(c).row_tiles(16);
+    const int64_t cols = stream_columns(tiles, TN);
+    const Way way = stream_way(c, WK);
+    return launch(way == Way::LDS    ? fp4_stream_kernel<A, CT, WK, WC, Way::LDS>
+                  : way == Way::ROWS ? fp4_stream_kernel<A, CT, WK, WC, Way::ROWS>
+                                     : fp4_stream_kernel<A, CT, WK, WC, Way::SHIFTED>,
+                  dim3((unsigned)(tiles * cols)), dim3(WK * WC * kWave), stream, c, TN, cols);
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
@@ -694,23 +791,24 @@ hipError_t run_tile(const Fp4Call& c, hipStream_t stream)
 }
 
 template <typename A, int BN, int BM, int WN, int WM>
-hipError_t run_ring(const Fp4Call& c, hipStream_t stream)
+hipError_t run_ring(const Fp4Call& c, int slices, hipStream_t stream)
 {
-    const int64_t TN = (c.n + BN - 1) / BN, groups = TN * shape_of(c).row_tiles(BM);
-    return launch(fp4_ring_kernel<A, BN, BM, WN, WM, ring_depth(BN, BM)>, dim3((unsigned)groups),
-                  dim3(WN * WM * kWave), stream, c, TN);
+    const int64_t TN = (c.n + BN - 1) / BN, tiles = TN * shape_of(c).row_tiles(BM);
+    const hipError_t status = launch(fp4_ring_kernel<A, BN, BM, WN, WM, ring_depth(BN, BM), ring_units(BM)>, dim3((unsigned)(tiles * slices)),
+                                     dim3(WN * WM * kWave), stream, c, TN, tiles, slices);
+    if (status != hipSuccess || slices == 1)
+        return status;
+    const int64_t items = c.m * (parts_row(c.n) / 4);
+    return launch(fp4_join_kernel<A>, dim3((unsigned)((items + kJoinThreads - 1) / kJoinThreads)), dim3(kJoinThreads), stream,
+                  c, slices);
 }
 
-template <typename A, int W>
+template <typename A>
 hipError_t run_streams(const Fp4Call& c, const Fp4Plan& p, hipStream_t stream)
 {
-    if (p.b == 1)
-        return p.a == 4   ? run_stream<A, 4, 1, W>(c, stream)
-               : p.a == 2 ? run_stream<A, 2, 1, W>(c, stream)
-                          : run_stream<A, 1, 1, W>(c, stream);
-    if (p.b == 2)
-        return p.a == 2 ? run_stream<A, 2, 2, W>(c, stream) : run_stream<A, 1, 2, W>(c, stream);
-    return run_stream<A, 1, 4, W>(c, stream);
+    return p.c == 4 ? run_stream<A, 2, 1, 4>(c, stream)
+           : p.c == 2 ? run_stream<A, 2, 2, 2>(c, stream)
+                      : run_stream<A, 1, 4, 1>(c, stream);
 }
 
 template <typename A>
@@ -718,23 +816,20 @@ hipError_t launch_typed(const Fp4Call& c, hipStream_t stream)
 {
     const Fp4Plan p = fp4_plan(shape_of(c), c.x, c.q, c.block_scale);
     if (p.kind == Fp4Kind::STREAM)
-        return p.w == 8 ? run_streams<A, 8>(c, p, stream) : run_streams<A, 4>(c, p, stream);
+        return run_streams<A>(c, p, stream);
     if (p.kind == Fp4Kind::TILE)
         return p.a == 256   ? run_tile<A, 256, 128, 2, 4>(c, stream)
                : p.b == 32  ? run_tile<A, 128, 32, 4, 1>(c, stream)
                : p.a == 128 ? run_tile<A, 128, 64, 2, 2>(c, stream)
                             : run_tile<A, 64, 64, 2, 2>(c, stream);
     if (p.b == 256)
-        return run_ring<A, 256, 256, 4, 2>(c, stream);
+        return run_ring<A, 256, 256, 4, 2>(c, p.slices, stream);
     if (p.b == 128)
-        return p.a == 256 ? run_ring<A, 256, 128, 4, 2>(c, stream) : run_ring<A, 128, 128, 4, 2>(c, stream);
+        return p.a == 256 ? run_ring<A, 256, 128, 4, 2>(c, p.slices, stream)
+                          : run_ring<A, 128, 128, 4, 2>(c, p.slices, stream);
     if (p.b == 64)
-        return p.a == 256   ? run_ring<A, 256, 64, 4, 2>(c, stream)
-               : p.a == 128 ? run_ring<A, 128, 64, 2, 2>(c, stream)
-                            : run_ring<A, 64, 64, 2, 2>(c, stream);
-    return p.a == 256   ? run_ring<A, 256, 32, 4, 1>(c, stream)
-           : p.a == 128 ? run_ring<A, 128, 32, 4, 1>(c, stream)
-                        : run_ring<A, 64, 32, 2, 1>(c, stream);
+        return p.a == 128 ? run_ring<A, 128, 64, 2, 2>(c, p.slices, stream) : run_ring<A, 64, 64, 2, 2>(c, p.slices, stream);
+    return p.a == 128 ? run_ring<A, 128, 32, 4, 1>(c, p.slices, stream) : run_ring<A, 64, 32, 2, 1>(c, p.slices, stream);
 }
 
 }  // namespace
@@ -744,9 +839,10 @@ hipError_t launch_fp4(const Fp4Call& c, Act act, hipStream_t stream)
     return act == Act::BF16 ? launch_typed<Bf16>(c, stream) : launch_typed<F16>(c, stream);
 }
 
-size_t linear_fp4_workspace_bytes(const Fp4Shape&, const void*, const uint8_t*, const uint8_t*)
+size_t linear_fp4_workspace_bytes(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale)
 {
-    return 0;
+    const Fp4Plan p = fp4_plan(s, x, q, scale);
+    return p.slices > 1 ? (size_t)(p.slices * s.m * parts_row(s.n)) * sizeof(float) : 0;
 }
 
 const char* fp4_kernel_name(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale)
@@ -754,10 +850,10 @@ const char* fp4_kernel_name(const Fp4Shape& s, const void* x, const uint8_t* q, 
     thread_local char name[96];
     const Fp4Plan p = fp4_plan(s, x, q, scale);
     if (p.kind == Fp4Kind::STREAM)
-        snprintf(name, sizeof name, "fp4_stream_kernel<CT=%d,RT=%d,W=%d>", p.a, p.b, p.w);
+        snprintf(name, sizeof name, "fp4_stream_kernel<CT=%d,WK=%d,WC=%d>", p.a, p.w, p.c);
     else
-        snprintf(name, sizeof name, "fp4_%s_kernel<BN=%d,BM=%d,W=%d>", p.kind == Fp4Kind::TILE ? "tile" : "ring", p.a,
-                 p.b, p.w);
+        snprintf(name, sizeof name, "fp4_%s_kernel<BN=%d,BM=%d,W=%d>,slices=%d", p.kind == Fp4Kind::TILE ? "tile" : "ring",
+                 p.a, p.b, p.w, p.slices);
     return name;
 }
 

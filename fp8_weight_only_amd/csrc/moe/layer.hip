@@ -1,16 +1,14 @@
 // A whole mixture-of-experts layer for a few tokens (t <= 64), two launches:
-//   h[s, i]  = silu(g) * u of slot s = token * top + j, g and u the gate and up
-//              products of token s / top with its j-th expert's rows i and inner + i
-//   out[t, c] = sum_j weights[t, j] * (sum_i h[s, i] * down[expert, c, i] + bias)
-// The choice and the weights are the router's (choose.hpp). Weights are e4m3 codes
+//   h[s, i]  = silu(g) * u, for each place s of a token with an expert: g and u the
+//              products of the token with the expert's rows i and inner + i
+//   out[t, c] = sum over t's places of weight * (sum_i h[s, i] * down[expert, c, i] + bias)
+// The choice and the weights are the router's. Weights are e4m3 codes
 // with a scale per output channel, or 4-bit codes with block scales (fp4.hpp).
 //
-// First launch: every workgroup chooses for all tokens (a few microseconds at most,
-// under the other workgroups' loads) rather than wait for a launch that does, and
-// makes the lists of the active experts and their slots in LDS. Its items are
-// 16 CT channels of one active expert, gate and up rows together, with all the
-// expert's rows (up to 64), so every weight is read once. The first workgroup
-// leaves choices and weights for the second launch.
+// First launch: every workgroup chooses for all tokens rather than wait for a launch
+// that does. Its items are 16 CT channels of one active expert, gate and up rows
+// together, with all the expert's rows (up to 64), so every weight is read once. The
+// first workgroup leaves the plan for the second launch.
 //
 // Second launch: a workgroup owns 16 CT output channels of every token. The active
 // experts' blocks of k, in one line, are split evenly over its waves; a wave adds
@@ -24,476 +22,581 @@
 #include <stdio.h>
 
 #include "choose.hpp"
-#include "fp4.hpp"
 #include "groups.hpp"
+#include "stream.hpp"
+#include "tile.hpp"
 
 namespace fp8w {
 namespace {
 
-constexpr int kMaxSlots = kMaxLayerTokens * kMaxTop;
-
-struct E4m3 {
-    static constexpr bool kBlockScales = false;
-    static constexpr int kUnit = 64;   // k of a 16-byte load by the four lane groups
-    static constexpr int kParts = 2;   // matrix instructions of a unit
-    __device__ static int64_t row_bytes(int64_t k) { return k; }
-    template <typename A>
-    __device__ __forceinline__ static u32x4 values(u32x4 v, int part, float)
-    {
-        const u32x2 a = A::decode4(part ? v.z : v.x), b = A::decode4(part ? v.w : v.y);
-        return u32x4{a.x, a.y, b.x, b.y};
-    }
-};
-
-struct Fp4 {
-    static constexpr bool kBlockScales = true;
-    static constexpr int kUnit = 128;
-    static constexpr int kParts = 4;
-    __device__ static int64_t row_bytes(int64_t k) { return (k + 1) / 2; }
-    template <typename A>
-    __device__ __forceinline__ static u32x4 values(u32x4 v, int part, float scale)
-    {
-        return decode_fp4<A>(part == 0 ? v.x : (part == 1 ? v.y : (part == 2 ? v.z : v.w)), scale);
-    }
-};
-
-typedef uint32_t u32_any __attribute__((aligned(1)));
-
-// NT tiles of 16 weight rows times RC tiles of 16 activation rows, straight from
-// memory into operand registers; the next block's loads run under a block's
-// products. A block is two units of k (one where the rows' registers would not
-// leave room for two).
-template <typename F, typename A, int NT, int RC, bool SHIFT, bool XSHIFT>
-struct Product {
-    static constexpr int U = RC == 1 ? 2 : 1, BK = U * F::kUnit, LANE = F::kUnit / 4;
-    Row<SHIFT> w[NT];
-    Row<XSHIFT> x[RC];
-    const uint8_t* s[NT];
-    int64_t k;
-    int g;
-    struct Block {
-        typename Row<SHIFT>::Raw w[NT][U];
-        typename Row<XSHIFT>::Raw x[RC][U][F::kParts];
-        uint32_t s[F::kBlockScales ? NT : 1][U];
+// A wave's choices for U tokens, lane r the r-th of each (-1: none) and its weight,
+// as route's: a lane holds the keys of experts lane, lane + 64, ..; a choice is the
+// largest key, of equal ones the lowest expert's. Short code rather than few
+// instructions: it runs once, on a cold instruction cache.
+template <int J, int U>
+__device__ __forceinline__ void choose_keys(const LayerCall& c, int token, float (&weight)[U], int (&id)[U])
+{
+    const int lane = threadIdx.x & 63, e = (int)c.e;
+    float l[U][J];
+    uint32_t key[U][J], mine[U], peak[U];
+    auto load = [&](auto&& get) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t row = (int64_t)(token + u < (int)c.t ? token + u : (int)c.t - 1) * e;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                l[u][j] = get(row + (lane + 64 * j < e ? lane + 64 * j : e - 1));
+        }
     };
-
-    __device__ __forceinline__ void weight_row(int t, const uint8_t* q, const void* scale, int64_t row)
-    {
-        w[t] = Row<SHIFT>(q + row * F::row_bytes(k) + 16 * g);
-        if constexpr (F::kBlockScales)
-            s[t] = static_cast<const uint8_t*>(scale) + row * ((k + 31) / 32);
-    }
-    __device__ __forceinline__ void x_row(int u, const void* p, int64_t first)
-    {
-        x[u] = Row<XSHIFT>(static_cast<const uint8_t*>(p) + 2 * (first + LANE * g));
-    }
-    __device__ __forceinline__ void load(Block& b, int64_t kb) const
-    {
-        if constexpr (F::kBlockScales)
+    if (c.logits_type == Act::FP32)
+        load([&](int64_t at) { return static_cast<const float*>(c.logits)[at]; });
+    else if (c.logits_type == Act::BF16)
+        load([&](int64_t at) { return Bf16::to_f32(static_cast<const uint16_t*>(c.logits)[at]); });
+    else
+        load([&](int64_t at) { return F16::to_f32(static_cast<const uint16_t*>(c.logits)[at]); });
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+    for (int u = 0; u < U; ++u) {
+        mine[u] = peak[u] = 0;
+        id[u] = -1;
 #pragma unroll
-                for (int h = 0; h < U; ++h)
-                    b.s[t][h] = *reinterpret_cast<const u32_any*>(s[t] + kb / 32 + 4 * h);
-#pragma unroll
-        for (int h = 0; h < U; ++h) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                b.w[t][h] = w[t].load(F::row_bytes(kb) + 64 * h);
-#pragma unroll
-            for (int u = 0; u < RC; ++u)
-#pragma unroll
-                for (int p = 0; p < F::kParts; ++p)
-                    b.x[u][h][p] = x[u].load(2 * (kb + F::kUnit * h) + 16 * p);
+        for (int j = 0; j < J; ++j) {
+            l[u][j] = lane + 64 * j < e ? l[u][j] : -INFINITY;
+            key[u][j] = key_of(l[u][j]);
         }
     }
-    __device__ __forceinline__ void products(const u32x4 (&v)[NT], const float (&scale)[NT],
-                                             const u32x4 (&xs)[RC][F::kParts], f32x4 (&acc)[NT][RC]) const
-    {
-#pragma unroll
-        for (int p = 0; p < F::kParts; ++p)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const u32x4 a = F::template values<A>(v[t], p, scale[t]);
-#pragma unroll
-                for (int u = 0; u < RC; ++u)
-                    acc[t][u] = A::mfma(a, xs[u][p], acc[t][u]);
-            }
-    }
-    __device__ __forceinline__ void compute(const Block& b, f32x4 (&acc)[NT][RC]) const
-    {
-#pragma unroll
-        for (int h = 0; h < U; ++h) {
-            u32x4 v[NT], xs[RC][F::kParts];
-            float scale[NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                v[t] = w[t].bytes(b.w[t][h]);
-                scale[t] = F::kBlockScales ? fp4_scale((b.s[F::kBlockScales ? t : 0][h] >> (8 * g)) & 255u) : 1.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < RC; ++u)
-#pragma unroll
-                for (int p = 0; p < F::kParts; ++p)
-                    xs[u][p] = x[u].bytes(b.x[u][h][p]);
-            products(v, scale, xs, acc);
-        }
-    }
-    // what is left of k behind the whole blocks
-    __device__ __forceinline__ void tail(int64_t kb, f32x4 (&acc)[NT][RC]) const
-    {
 #pragma unroll 1
-        for (int h = 0; h < U; ++h) {
-            const int64_t left = k - kb - F::kUnit * h - LANE * g;
-            u32x4 v[NT], xs[RC][F::kParts];
-            float scale[NT];
+    for (int r = 0; r < c.top; ++r) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if constexpr (F::kBlockScales) {
-                    v[t] = first_codes(w[t].part(F::row_bytes(kb) + 64 * h, (left + 1) / 2), left);
-                    scale[t] = fp4_scale(left > 0 ? s[t][kb / 32 + 4 * h + g] : 127);
-                } else {
-                    v[t] = w[t].part(kb + 64 * h, left);
-                    scale[t] = 1.0f;
-                }
+        for (int u = 0; u < U; ++u) {
+            uint32_t head = key[u][0];
+#pragma unroll
+            for (int j = 1; j < J; ++j)
+                head = head > key[u][j] ? head : key[u][j];
+            const uint32_t best = wave_max_u32(head);
+            int expert = 0;
+#pragma unroll
+            for (int j = J - 1; j >= 0; --j) {
+                const uint64_t has = __ballot(key[u][j] == best);
+                expert = has ? 64 * j + (int)__builtin_ctzll(has) : expert;
             }
 #pragma unroll
-            for (int u = 0; u < RC; ++u)
+            for (int j = 0; j < J; ++j)
+                key[u][j] = lane + 64 * j == expert ? 0 : key[u][j];
+            peak[u] = r == 0 ? best : peak[u];
+            const bool take = lane == r && best != 0;
+            mine[u] = take ? best : mine[u];
+            id[u] = take ? expert : id[u];
+        }
+    }
 #pragma unroll
-                for (int p = 0; p < F::kParts; ++p)
-                    xs[u][p] = x[u].part(2 * (kb + F::kUnit * h) + 16 * p, 2 * left - 16 * p);
-            products(v, scale, xs, acc);
+    for (int u = 0; u < U; ++u) {
+        const float top_logit = logit_of(peak[u]);
+        float num = mine[u] ? expf(logit_of(mine[u]) - top_logit) : 0.0f, part = num;
+        if (!c.renorm) {
+            part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                part += l[u][j] == -INFINITY ? 0.0f : expf(l[u][j] - top_logit);
         }
+        const float total = group_sum<kWave>(part);
+        weight[u] = id[u] >= 0 ? num / total : 0.0f;
     }
-    // blocks b, b + step, .. below end (all of them the same in every lane)
-    __device__ __forceinline__ void run(int64_t b, int64_t end, int step, f32x4 (&acc)[NT][RC]) const
-    {
-        const int64_t whole = k / BK, last = end < whole ? end : whole;
-        int64_t i = b;
-        if (i < last) {
-            Block cur;
-            load(cur, BK * i);
-            for (i += step; i < last; i += step) {
-                Block next;
-                load(next, BK * i);
-                compute(cur, acc);
-                cur = next;
+}
+
+template <int U>
+__device__ __forceinline__ void choose_by_wave(const LayerCall& c, int token, float (&weight)[U], int (&id)[U])
+{
+    if (c.e <= 64)
+        choose_keys<1, U>(c, token, weight, id);
+    else if (c.e <= 128)
+        choose_keys<2, U>(c, token, weight, id);
+    else if (c.e <= 256)
+        choose_keys<4, U>(c, token, weight, id);
+    else
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            float w[1];
+            int i[1];
+            choose_keys<16, 1>(c, token + u, w, i);
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                weight[q] = u == q ? w[0] : weight[q];
+                id[q] = u == q ? i[0] : id[q];
             }
-            compute(cur, acc);
         }
-        if (i == whole && whole < end && BK * whole < k)
-            tail(BK * whole, acc);
-    }
+}
+
+// What the first launch leaves for the second: the active experts in order, their first
+// rows and each row's token and weight, and the choices by token, for the biases. A row
+// is a token's place with one expert; an expert's rows stand by rising token.
+//
+// h keeps an expert's rows in groups of four, eight values of each in turn: group G has
+// value i of its row b at (G * pitch + i / 8 * 8) * 4 + 8 b + i % 8 (stream.hpp).
+struct Plan {
+    int32_t *count, *active, *start, *group, *token, *choice;
+    float *weight, *share;
 };
 
-// The active experts in order, each one's slots, in LDS.
-struct Lists {
-    int cursor[kMaxExperts];
-    int16_t id[kMaxSlots];
-    uint16_t row[kMaxSlots];
-    uint16_t active[kMaxExperts], start[kMaxExperts + 1];
-    int count;
+// Rows that are multiplied together: an expert with more (t > 32 only) stands in the
+// plan again for the next ones, and its weights are read again.
+constexpr int kRows = 32;
+constexpr int kMaxEntries = kMaxExperts + kMaxLayerTokens * kMaxTop / kRows;
 
-    template <int NT>
-    __device__ __forceinline__ void clear(int e)
-    {
-        for (int i = threadIdx.x; i < e; i += NT)
-            cursor[i] = 0;
-    }
-    // From id[] and the experts' counts in cursor[], both written before a barrier. An
-    // expert's slots stand in any order: a slot's sums do not depend on its place.
-    template <int NT>
-    __device__ __forceinline__ void build(int slots, int e)
-    {
-        if (threadIdx.x < kWave) {
-            const int lane = threadIdx.x;
-            int experts = 0, rows = 0;
-            for (int i0 = 0; i0 < e; i0 += kWave) {
-                const int i = i0 + lane, n = i < e ? cursor[i] : 0, incl = wave_prefix(n);
-                const uint64_t on = __ballot(n > 0);
-                if (n > 0) {
-                    const int at = experts + __popcll(on & (((uint64_t)1 << lane) - 1));
-                    active[at] = (uint16_t)i;
-                    start[at] = (uint16_t)(rows + incl - n);
-                    cursor[i] = rows + incl - n;
+__device__ __host__ inline int64_t most_entries(int64_t t, int64_t e, int64_t top)
+{
+    const int64_t slots = t * top;
+    return (slots < e ? slots : e) + (t > kRows ? slots / kRows : 0);
+}
+
+// Rows of h: every entry's last group may have up to three of no token.
+__device__ __host__ inline int64_t h_rows(int64_t t, int64_t e, int64_t top)
+{
+    return t * top + 3 * most_entries(t, e, top);
+}
+
+__device__ __host__ inline Plan plan_of(const LayerCall& c)
+{
+    const int64_t slots = c.t * c.top, most = most_entries(c.t, c.e, c.top);
+    Plan p;
+    p.count = c.plan;
+    p.active = p.count + 1;
+    p.start = p.active + most;
+    p.group = p.start + most + 1;
+    p.token = p.group + most;
+    p.choice = p.token + slots;
+    p.weight = reinterpret_cast<float*>(p.choice + slots);
+    p.share = p.weight + slots;
+    return p;
+}
+
+constexpr int kPlanNumbers = 4;  // per slot, besides 2 and 3 per expert
+
+// LDS of the first launch: the tokens of every expert as bits (t <= 64), the active
+// experts and their first rows. The first workgroup's choices, for the plan, stand where
+// the stream begins afterwards.
+struct Lists {
+    uint64_t tokens[kMaxExperts];
+    uint16_t active[kMaxEntries], start[kMaxEntries + 1], group[kMaxEntries], of[kMaxExperts];
+    int count;
+};
+template <int SLOTS>
+struct Choices {
+    float weight[SLOTS];
+    int16_t id[SLOTS];
+};
+
+// The token of row `lane` of an expert whose tokens are these bits.
+__device__ __forceinline__ int token_of_row(uint64_t tokens)
+{
+    const int lane = threadIdx.x & 63;
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    const int to = (tokens >> lane) & 1 ? __popcll(tokens & below) : __popcll(tokens) + __popcll(~tokens & below);
+    return __builtin_amdgcn_ds_permute(4 * to, lane);  // a permutation: every lane is written once
+}
+
+// An item is 16 CT channels of gate and of up of one active expert; a workgroup has
+// every gridDim.x-th. Its W waves take the steps of k in turn. A wave's loads run a step
+// ahead, into the next item while this one's sums meet in LDS, so the stream of weights
+// does not stop between items.
+//
+// RC: tiles of 16 rows (0: one token, whose choices every wave makes for itself, with
+// no barrier before the first loads).
+template <typename F, typename A, int CT, int RC, int W, Way WAY>
+__global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int TN)
+{
+    constexpr int NT = W * kWave, CH = 16 * CT, RT = RC == 0 ? 1 : RC;
+    static_assert(NT % CH == 0, "a thread's values are of one channel");
+    constexpr bool ONE = RC == 0;
+    constexpr int SLOTS = (RC <= 1 ? 16 : kMaxLayerTokens) * kMaxTop;
+    using S = Stream<F, A, 2 * CT, 2, RT, WAY, false>;
+    using C = Choices<SLOTS>;
+    constexpr size_t kRing = (size_t)W * S::LDS, kChoices = ONE ? 16 : sizeof(C);
+    __shared__ std::conditional_t<ONE, char, Lists> lists;
+    __shared__ __attribute__((aligned(16))) uint8_t ring[kRing > kChoices ? kRing : kChoices];
+    __shared__ __attribute__((aligned(16))) float part[W][2 * CT][4 * kWave];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const Plan plan = plan_of(c);
+    int count, one_id = -1;
+    if constexpr (ONE) {
+        float weight[1];
+        int id[1];
+        choose_by_wave<1>(c, 0, weight, id);
+        one_id = id[0];
+        count = __popcll(__ballot(one_id >= 0));
+        if (blockIdx.x == 0 && wave == 0) {
+            if (lane == 0) {
+                *plan.count = count;
+                plan.start[0] = 0;
+            }
+            if (lane < count) {
+                plan.active[lane] = one_id;
+                plan.start[lane + 1] = lane + 1;
+                plan.group[lane] = lane;
+                plan.token[lane] = 0;
+                plan.weight[lane] = weight[0];
+            }
+            if (lane < c.top) {
+                plan.choice[lane] = one_id;
+                plan.share[lane] = weight[0];
+            }
+        }
+    } else {
+        const int e = (int)c.e, slots = (int)c.t * c.top;
+        C& mine = *reinterpret_cast<C*>(ring);
+        for (int i = tid; i < e; i += NT)
+            lists.tokens[i] = 0;
+        __syncthreads();
+#pragma unroll 1
+        for (int t = 2 * wave; t < (int)c.t; t += 2 * W) {
+            float weight[2];
+            int id[2];
+            choose_by_wave<2>(c, t, weight, id);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (t + u < (int)c.t && lane < c.top) {
+                    if (id[u] >= 0)
+                        atomicOr(reinterpret_cast<uint32_t*>(&lists.tokens[id[u]]) + ((t + u) >> 5), 1u << ((t + u) & 31));
+                    if (blockIdx.x == 0) {
+                        const int s = (t + u) * c.top + lane;
+                        mine.id[s] = (int16_t)id[u];
+                        mine.weight[s] = weight[u];
+                        plan.choice[s] = id[u];
+                        plan.share[s] = weight[u];
+                    }
                 }
-                experts += __popcll(on);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            int experts = 0, rows = 0, groups = 0;
+#pragma unroll 1
+            for (int i0 = 0; i0 < e; i0 += kWave) {
+                const int i = i0 + lane, n = i < e ? __popcll(lists.tokens[i]) : 0, incl = wave_prefix(n);
+                const int entries = (n + 16 * RT - 1) / (16 * RT), upto = wave_prefix(entries);
+                const int fours = wave_prefix((n + 3) / 4);
+                if (n > 0) {
+                    const int at = experts + upto - entries, row = rows + incl - n;
+                    lists.of[i] = (uint16_t)row;
+                    for (int q = 0; q < entries; ++q) {
+                        lists.active[at + q] = (uint16_t)i;
+                        lists.start[at + q] = (uint16_t)(row + 16 * RT * q);
+                        lists.group[at + q] = (uint16_t)(groups + fours - (n + 3) / 4 + 4 * RT * q);
+                    }
+                }
+                experts += __builtin_amdgcn_readlane(upto, 63);
                 rows += __builtin_amdgcn_readlane(incl, 63);
+                groups += __builtin_amdgcn_readlane(fours, 63);
             }
             if (lane == 0) {
-                start[experts] = (uint16_t)rows;
-                count = experts;
+                lists.start[experts] = (uint16_t)rows;
+                lists.count = experts;
             }
         }
         __syncthreads();
-        for (int s = threadIdx.x; s < slots; s += NT)
-            if (id[s] >= 0)
-                row[atomicAdd(&cursor[id[s]], 1)] = (uint16_t)s;
-        __syncthreads();
-    }
-};
-
-// f(integral_constant<int, RC>) for the row tiles that `rows` rows need.
-template <int RCMAX, typename Fn>
-__device__ __forceinline__ void with_row_tiles(int rows, Fn&& f)
-{
-    if constexpr (RCMAX > 1) {
-        if (rows > 32)
-            return f(std::integral_constant<int, 4>{});
-        if (rows > 16)
-            return f(std::integral_constant<int, 2>{});
-    }
-    f(std::integral_constant<int, 1>{});
-}
-
-__device__ __forceinline__ float channel_scale(const void* scale, int64_t at)
-{
-    return static_cast<const float*>(scale)[at];
-}
-
-template <int WAVES, typename Fn>
-__device__ __forceinline__ void choose_all(const LayerCall& c, Fn&& done)
-{
-#define FP8W_CHOOSE(G, J) \
-    return choose_chunk<G, J, WAVES>(c.logits, c.logits_type, 0, c.t, (int)c.e, c.top, c.renorm != 0, done)
-    if (choice_lanes(c.e, c.top) == 16) {
-        if (c.e <= 16)
-            FP8W_CHOOSE(16, 1);
-        FP8W_CHOOSE(16, 4);
-    }
-    if (c.e <= 64)
-        FP8W_CHOOSE(64, 1);
-    if (c.e <= 128)
-        FP8W_CHOOSE(64, 2);
-    if (c.e <= 256)
-        FP8W_CHOOSE(64, 4);
-    FP8W_CHOOSE(64, 16);
-#undef FP8W_CHOOSE
-}
-
-template <typename F, typename A, int CT, int RCMAX, int W, bool SHIFT>
-__global__ __launch_bounds__(W* kWave) void layer_up_kernel(LayerCall c, int TN)
-{
-    constexpr int NT = W * kWave;
-    __shared__ Lists lists;
-    __shared__ __attribute__((aligned(16))) f32x4 part[W][2 * CT][kWave];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int slots = (int)c.t * c.top;
-    lists.clear<NT>((int)c.e);
-    __syncthreads();
-    choose_all<W>(c, [&](int64_t tok, int j, int id, float weight) {
-        const int s = (int)tok * c.top + j;
-        lists.id[s] = (int16_t)id;
-        if (id >= 0)
-            atomicAdd(&lists.cursor[id], 1);
+        count = uniform(lists.count);
         if (blockIdx.x == 0) {
-            c.ids[s] = id;
-            c.weights[s] = weight;
-        }
-    });
-    __syncthreads();
-    lists.build<NT>(slots, (int)c.e);
-    const int items = TN * uniform(lists.count);
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int a = uniform(it / TN), expert = uniform(lists.active[a]), first = uniform(lists.start[a]);
-        const int rows = uniform(lists.start[a + 1]) - first;
-        const int64_t n0 = (int64_t)(it - a * TN) * (16 * CT), up = (int64_t)expert * 2 * c.inner;
-        with_row_tiles<RCMAX>(rows, [&](auto rc) {
-            constexpr int RC = decltype(rc)::value;
-            Product<F, A, 2 * CT, RC, SHIFT, SHIFT> p;
-            p.k = c.hidden;
-            p.g = g;
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const int64_t ch = n0 + 16 * t + r < c.inner ? n0 + 16 * t + r : c.inner - 1;
-                p.weight_row(t, c.up.q, c.up.scale, up + ch);
-                p.weight_row(CT + t, c.up.q, c.up.scale, up + c.inner + ch);
-            }
-#pragma unroll
-            for (int u = 0; u < RC; ++u) {
-                const int i = 16 * u + r < rows ? 16 * u + r : 0;  // rows past the expert's: any row, not stored
-                p.x_row(u, c.x, (int64_t)((uint32_t)lists.row[first + i] / (uint32_t)c.top) * c.hidden);
-            }
-            f32x4 acc[2 * CT][RC];
-#pragma unroll
-            for (int t = 0; t < 2 * CT; ++t)
-#pragma unroll
-                for (int u = 0; u < RC; ++u)
-                    acc[t][u] = f32x4{0.0f};
-            p.run(wave, (c.hidden + p.BK - 1) / p.BK, W, acc);
-#pragma unroll
-            for (int u = 0; u < RC; ++u) {
-#pragma unroll
-                for (int t = 0; t < 2 * CT; ++t)
-                    part[wave][t][lane] = acc[t][u];
-                __syncthreads();
-                // lane (r, g): channels 4 g .. 4 g + 3 of row r
-                for (int t = wave; t < CT; t += W) {
-                    f32x4 gs = part[0][t][lane], us = part[0][CT + t][lane];
-#pragma unroll
-                    for (int v = 1; v < W; ++v) {
-                        gs += part[v][t][lane];
-                        us += part[v][CT + t][lane];
-                    }
-                    const int64_t c0 = n0 + 16 * t + 4 * g;
-                    if (16 * u + r < rows && c0 < c.inner) {
-                        const float gv[4] = {gs.x, gs.y, gs.z, gs.w}, uv[4] = {us.x, us.y, us.z, us.w};
-                        const uint16_t* bias = static_cast<const uint16_t*>(c.up.bias);
-                        uint16_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int64_t gc = up + (c0 + i < c.inner ? c0 + i : c.inner - 1), uc = gc + c.inner;
-                            const float sg = F::kBlockScales ? 1.0f : channel_scale(c.up.scale, gc);
-                            const float su = F::kBlockScales ? 1.0f : channel_scale(c.up.scale, uc);
-                            const float gate = __builtin_fmaf(sg, gv[i], A::to_f32(bias_bits(bias, gc)));
-                            const float lift = __builtin_fmaf(su, uv[i], A::to_f32(bias_bits(bias, uc)));
-                            o[i] = rounded<A>(gate / (1.0f + expf(-gate)) * lift);
-                        }
-                        const u32x2 pk{(uint32_t)o[0] | ((uint32_t)o[1] << 16), (uint32_t)o[2] | ((uint32_t)o[3] << 16)};
-                        *reinterpret_cast<u32x2*>(c.h + lists.row[first + 16 * u + r] * c.pitch + c0) = pk;
-                    }
+            if (tid == 0)
+                *plan.count = count;
+            for (int i = tid; i <= count; i += NT) {
+                plan.start[i] = lists.start[i];
+                if (i < count) {
+                    plan.active[i] = lists.active[i];
+                    plan.group[i] = lists.group[i];
                 }
-                __syncthreads();
             }
+            for (int s = tid; s < slots; s += NT) {
+                const int id = mine.id[s], tok = s / c.top;
+                if (id >= 0) {
+                    const int at = lists.of[id] + __popcll(lists.tokens[id] & (((uint64_t)1 << tok) - 1));
+                    plan.token[at] = tok;
+                    plan.weight[at] = mine.weight[s];
+                }
+            }
+            __syncthreads();
+        }
+    }
+
+    S st(c.hidden, c.x, 2 * c.t * c.hidden, ring + wave * S::LDS);
+    struct Item {
+        int group, rows;
+        int64_t n0, up;  // first channel; the expert's first gate row
+    };
+    const int items = TN * count, NU = (st.steps + W - 1) / W;  // steps of a wave in an item
+    auto enter = [&](int it, Item& item, typename S::Source& src) {
+        const int a = uniform(it / TN);
+        int expert, tok = 0, before = 0;  // the expert's rows before the item's
+        item.group = a;
+        item.rows = 1;
+        if constexpr (ONE) {
+            expert = __builtin_amdgcn_readlane(one_id, a);
+        } else {
+            expert = uniform(lists.active[a]);
+            const int first = uniform(lists.start[a]);
+            item.group = uniform(lists.group[a]);
+            item.rows = uniform(lists.start[a + 1]) - first;
+            before = first - uniform(lists.of[expert]);
+            tok = token_of_row(lists.tokens[expert]);
+        }
+        item.n0 = (int64_t)(it - a * TN) * CH;
+        item.up = (int64_t)expert * 2 * c.inner;
+        st.weights(src, 0, c.up.q, c.up.scale, item.up + item.n0, 2 * c.e * c.inner);
+        st.weights(src, 1, c.up.q, c.up.scale, item.up + c.inner + item.n0, 2 * c.e * c.inner);
+        // rows past the item's: any row, not stored
+        st.rows(src, item.rows, [&](int i) {
+            return ONE ? 0 : (int64_t)__shfl(tok, before + (i < item.rows ? i : 0), kWave) * c.hidden;
         });
+    };
+    int it = blockIdx.x;
+    if (it >= items)
+        return;
+    Item item, next;
+    typename S::Source src;
+    enter(it, item, src);
+    st.load(src, wave, wave < st.steps);
+#pragma unroll 1
+    for (; it < items; it += gridDim.x, item = next) {
+        // the scales and biases of this thread's channel
+        const int ch = tid % CH, channels = (int)(c.inner - item.n0 < CH ? c.inner - item.n0 : CH);
+        const int64_t gc = item.up + item.n0 + (ch < channels ? ch : 0), uc = gc + c.inner;
+        const uint16_t* bias = static_cast<const uint16_t*>(c.up.bias);
+        const float* scale = static_cast<const float*>(c.up.scale);
+        const float gs = F::kBlockScales ? 1.0f : scale[gc], us = F::kBlockScales ? 1.0f : scale[uc];
+        const uint16_t gb = bias_bits(bias, gc), ub = bias_bits(bias, uc);
+        f32x4 acc[2 * CT][RT];
+#pragma unroll
+        for (int t = 0; t < 2 * CT; ++t)
+#pragma unroll
+            for (int u = 0; u < RT; ++u)
+                acc[t][u] = f32x4{0.0f};
+#pragma unroll 1
+        for (int v = 0; v < NU; ++v) {
+            int ahead = v + 1;
+            bool more = true;
+            if (ahead == NU) {
+                ahead = 0;
+                more = it + (int)gridDim.x < items;
+                if (more)
+                    enter(it + gridDim.x, next, src);
+            }
+            ahead = wave + W * ahead;
+            st.consume(wave + W * v, src, ahead, more && ahead < st.steps, acc);
+        }
+#pragma unroll 1
+        for (int u = 0; u < RT; ++u) {
+            if (16 * u >= item.rows)
+                break;
+#pragma unroll
+            for (int t = 0; t < 2 * CT; ++t) {
+                f32x4 sums = acc[t][0];
+#pragma unroll
+                for (int q = 1; q < RT; ++q)
+                    sums = u == q ? acc[t][q] : sums;
+                *reinterpret_cast<f32x4*>(&part[wave][t][4 * lane]) = sums;
+            }
+            lds_barrier();
+            // lane (r, g) of a tile has its channels 4 g .. 4 g + 3 of row r
+            const int here = item.rows - 16 * u < 16 ? item.rows - 16 * u : 16;
+#pragma unroll 1
+            for (int row = tid / CH; row < here; row += NT / CH) {
+                const int at = 4 * (row + 16 * ((ch & 15) >> 2)) + (ch & 3);
+                float gate = 0.0f, lift = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    gate += part[w][ch / 16][at];
+                    lift += part[w][CT + ch / 16][at];
+                }
+                gate = __builtin_fmaf(gs, gate, A::to_f32(gb));
+                lift = __builtin_fmaf(us, lift, A::to_f32(ub));
+                const int64_t i = item.n0 + ch;
+                if (ch < channels)
+                    c.h[((item.group + 4 * u + row / 4) * c.pitch + i / 8 * 8) * 4 + 8 * (row & 3) + i % 8] =
+                        rounded<A>(gate / (1.0f + expf(-gate)) * lift);
+            }
+            lds_barrier();
+        }
     }
 }
 
-template <typename F, typename A, int CT, int RCMAX, int W, bool SHIFT>
+// A workgroup has 16 output channels of every token. A wave's steps run over the active
+// experts; at an expert's end (or the wave's own) its sums go to the wave's accumulators
+// of the tokens.
+template <typename F, typename A, int RC, int W, Way WAY>
 __global__ __launch_bounds__(W* kWave) void layer_down_kernel(LayerCall c)
 {
-    constexpr int NT = W * kWave, TOKENS = 16 * RCMAX;
-    __shared__ Lists lists;
-    __shared__ float weight[RCMAX == 1 ? 16 * kMaxTop : kMaxSlots];
-    __shared__ __attribute__((aligned(16))) f32x4 sum[W][TOKENS][4 * CT];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int slots = (int)c.t * c.top;
-    lists.clear<NT>((int)c.e);
-    for (int i = threadIdx.x; i < W * TOKENS * 4 * CT; i += NT)
+    constexpr int NT = W * kWave, RT = RC == 0 ? 1 : RC;
+    constexpr int TOKENS = RC == 0 ? 1 : (RC == 1 ? 16 : kMaxLayerTokens);
+    __shared__ __attribute__((aligned(16))) f32x4 sum[W][TOKENS][4];
+    __shared__ uint16_t active[kMaxEntries], start[kMaxEntries + 1], group[kMaxEntries];
+    __shared__ uint8_t token[TOKENS * kMaxTop];
+    __shared__ float weight[TOKENS * kMaxTop];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int slots = (int)c.t * c.top, most = (int)most_entries(c.t, c.e, c.top);
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const Plan plan = plan_of(c);
+    const int count = uniform(*plan.count);
+    // what lies behind the lists' ends is of no use, and not used
+    for (int i = tid; i <= most; i += NT) {
+        start[i] = (uint16_t)plan.start[i];
+        if (i < most) {
+            active[i] = (uint16_t)plan.active[i];
+            group[i] = (uint16_t)plan.group[i];
+        }
+    }
+    for (int i = tid; i < slots; i += NT) {
+        token[i] = (uint8_t)plan.token[i];
+        weight[i] = plan.weight[i];
+    }
+    for (int i = tid; i < W * TOKENS * 4; i += NT)
         (&sum[0][0][0])[i] = f32x4{0.0f};
     __syncthreads();
-    for (int s = threadIdx.x; s < slots; s += NT) {
-        const int id = c.ids[s];
-        lists.id[s] = (int16_t)id;
-        weight[s] = c.weights[s];
-        if (id >= 0)
-            atomicAdd(&lists.cursor[id], 1);
+    if (c.down.bias) {
+#pragma unroll 1
+        for (int i = tid; i < (int)c.t * 16; i += NT) {
+            float z = 0.0f;
+#pragma unroll 1
+            for (int j = 0; j < c.top && n0 + i % 16 < c.hidden; ++j) {
+                const int s = i / 16 * c.top + j, id = plan.choice[s];
+                if (id >= 0)
+                    z = __builtin_fmaf(plan.share[s], A::to_f32(static_cast<const uint16_t*>(
+                                                          c.down.bias)[id * c.hidden + n0 + i % 16]), z);
+            }
+            reinterpret_cast<float*>(&sum[0][i / 16][0])[i % 16] = z;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    lists.build<NT>(slots, (int)c.e);
-    const int64_t n0 = (int64_t)blockIdx.x * (16 * CT);
-    // this wave's blocks of two units among all experts'
-    const int per = (int)((c.inner + 2 * F::kUnit - 1) / (2 * F::kUnit)), all = per * uniform(lists.count);
-    const int hi = uniform(all * (wave + 1) / W);
-    for (int at = uniform(all * wave / W); at < hi;) {
-        const int a = uniform(at / per), b0 = at - a * per, b1 = b0 + hi - at < per ? b0 + hi - at : per;
-        at += b1 - b0;
-        const int expert = uniform(lists.active[a]), first = uniform(lists.start[a]);
-        const int rows = uniform(lists.start[a + 1]) - first;
-        with_row_tiles<RCMAX>(rows, [&](auto rc) {
-            constexpr int RC = decltype(rc)::value;
-            Product<F, A, CT, RC, SHIFT, false> p;
-            p.k = c.inner;
-            p.g = g;
+
+    using S = Stream<F, A, 1, 1, RT, WAY, true>;
+    __shared__ __attribute__((aligned(16))) uint8_t ring[W][S::LDS];
+    S st(c.inner, c.h, 2 * h_rows(c.t, c.e, c.top) * c.pitch, ring[wave]);
+    struct Source : S::Source {
+        Buffer scale;
+    } src;
+    const int per = st.steps, all = per * count;
+    const int lo = uniform((int)((int64_t)all * wave / W)), n = uniform((int)((int64_t)all * (wave + 1) / W)) - lo;
+    auto enter = [&](int a) {
+        const int expert = uniform(active[a]), rows = uniform(start[a + 1]) - uniform(start[a]), G = uniform(group[a]);
+        const int64_t row = (int64_t)expert * c.hidden + n0;
+        st.weights(src, 0, c.down.q, c.down.scale, row, c.e * c.hidden);
+        if constexpr (!F::kBlockScales)
+            src.scale = Buffer(static_cast<const float*>(c.down.scale) + row, 4 * (c.e * c.hidden - row));
+        st.rows(src, rows, [&](int i) { return (G + (i < rows ? i / 4 : 0)) * 4 * c.pitch; });
+    };
+    int la = uniform(lo / per), lp = lo - la * per, ca = la, cp = lp;  // the loads' expert and step, the products'
+    // the channels' scales where the expert's sums are added up, after step lp
+    auto load_scale = [&](bool on) {
+        u32x4 v{0, 0, 0, 0};
+        if constexpr (!F::kBlockScales)
+            v = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(src.scale.rsrc, 16 * g, src.scale.at(on, 0), 0));
+        return v;
+    };
+    u32x4 scale_bits{0, 0, 0, 0};
+    if (n > 0) {
+        enter(la);
+        scale_bits = load_scale(lp + 1 == per || n == 1);
+        st.load(src, lp, true);
+    }
+    f32x4 acc[1][RT];
 #pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const int64_t ch = n0 + 16 * t + r < c.hidden ? n0 + 16 * t + r : c.hidden - 1;
-                p.weight_row(t, c.down.q, c.down.scale, (int64_t)expert * c.hidden + ch);
+    for (int u = 0; u < RT; ++u)
+        acc[0][u] = f32x4{0.0f};
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+            const bool more = i + 1 < n;
+            if (++lp == per && more) {
+                lp = 0;
+                enter(++la);
             }
+            const u32x4 scale_next = load_scale(more && (lp + 1 == per || i + 2 == n));
+            st.consume(cp, src, lp, more, acc);
+            if (++cp == per || !more) {
+                const int first = uniform(start[ca]), rows = uniform(start[ca + 1]) - first;
+                const f32x4 scale = F::kBlockScales ? f32x4{1.0f, 1.0f, 1.0f, 1.0f} : __builtin_bit_cast(f32x4, scale_bits);
+                // lane (r, g): channels 4 g .. 4 g + 3 of row r; an expert has a token once
 #pragma unroll
-            for (int u = 0; u < RC; ++u) {
-                const int i = 16 * u + r < rows ? 16 * u + r : 0;
-                p.x_row(u, c.h, lists.row[first + i] * c.pitch);
-            }
-            f32x4 acc[CT][RC];
-#pragma unroll
-            for (int t = 0; t < CT; ++t)
-#pragma unroll
-                for (int u = 0; u < RC; ++u)
-                    acc[t][u] = f32x4{0.0f};
-            p.run(b0 * (2 / p.U), b1 * (2 / p.U), 1, acc);
-            // lane (r, g): channels 4 g .. 4 g + 3 of row r; an expert has a token once
-#pragma unroll
-            for (int t = 0; t < CT; ++t) {
-                const int64_t c0 = n0 + 16 * t + 4 * g;
-                float scale[4], bias[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t ch = (int64_t)expert * c.hidden + (c0 + i < c.hidden ? c0 + i : c.hidden - 1);
-                    scale[i] = F::kBlockScales ? 1.0f : channel_scale(c.down.scale, ch);
-                    bias[i] = b0 == 0 ? A::to_f32(bias_bits(static_cast<const uint16_t*>(c.down.bias), ch)) : 0.0f;
-                }
-#pragma unroll
-                for (int u = 0; u < RC; ++u) {
+                for (int u = 0; u < RT; ++u) {
                     if (16 * u + r < rows) {
-                        const int s = lists.row[first + 16 * u + r];
-                        const float wt = weight[s];
-                        f32x4& to = sum[wave][(uint32_t)s / (uint32_t)c.top][4 * t + g];
-                        const f32x4 v = acc[t][u];
+                        const int row = first + 16 * u + r;
+                        f32x4& to = sum[wave][TOKENS == 1 ? 0 : token[row]][g];
+                        const f32x4 v = acc[0][u];
+                        const float w = weight[row];
                         f32x4 z = to;
-                        z.x = __builtin_fmaf(wt, __builtin_fmaf(scale[0], v.x, bias[0]), z.x);
-                        z.y = __builtin_fmaf(wt, __builtin_fmaf(scale[1], v.y, bias[1]), z.y);
-                        z.z = __builtin_fmaf(wt, __builtin_fmaf(scale[2], v.z, bias[2]), z.z);
-                        z.w = __builtin_fmaf(wt, __builtin_fmaf(scale[3], v.w, bias[3]), z.w);
+                        z.x = __builtin_fmaf(w, scale.x * v.x, z.x);
+                        z.y = __builtin_fmaf(w, scale.y * v.y, z.y);
+                        z.z = __builtin_fmaf(w, scale.z * v.z, z.z);
+                        z.w = __builtin_fmaf(w, scale.w * v.w, z.w);
                         to = z;
                     }
+                    acc[0][u] = f32x4{0.0f};
                 }
+                wave_sync();
+                cp = 0;
+                ++ca;
             }
-            wave_sync();
-        });
+            scale_bits = scale_next;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < (int)c.t * 4 * CT; i += NT) {
-        const int tok = i / (4 * CT), q = i % (4 * CT);
-        f32x4 z = sum[0][tok][q];
+#pragma unroll 1
+    for (int i = tid; i < (int)c.t * 16; i += NT) {
+        const int tok = i / 16, ch = i % 16;
+        float z = reinterpret_cast<const float*>(&sum[0][tok][0])[ch];
 #pragma unroll
         for (int v = 1; v < W; ++v)
-            z += sum[v][tok][q];
-        const int64_t c0 = n0 + 4 * q;
-        const uint16_t o[4] = {rounded<A>(z.x), rounded<A>(z.y), rounded<A>(z.z), rounded<A>(z.w)};
-        if (c0 < c.hidden)
-            store4(static_cast<uint16_t*>(c.out) + tok * c.hidden + c0, o, c.hidden - c0);
+            z += reinterpret_cast<const float*>(&sum[v][tok][0])[ch];
+        if (n0 + ch < c.hidden)
+            static_cast<uint16_t*>(c.out)[tok * c.hidden + n0 + ch] = rounded<A>(z);
     }
 }
 
 // ------------------------------------------------------------------ plans
 constexpr int kUpGroups = 1024;
 
-bool rows_shifted(const void* a, const void* b, int64_t bytes)
-{
-    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | (uintptr_t)bytes) & 3) != 0;
-}
-
-template <typename F, typename A, int CT, int RCMAX, bool SHIFT>
+template <typename F, typename A, int CT, int RC, int W, Way WAY>
 hipError_t run_up(const LayerCall& c, hipStream_t stream)
 {
-    const int64_t TN = (c.inner + 16 * CT - 1) / (16 * CT), most = c.t * c.top < c.e ? c.t * c.top : c.e;
+    const int64_t TN = (c.inner + 16 * CT - 1) / (16 * CT), most = most_entries(c.t, c.e, c.top);
     const int64_t items = TN * most;
-    return launch(layer_up_kernel<F, A, CT, RCMAX, 8, SHIFT>, dim3((unsigned)(items < kUpGroups ? items : kUpGroups)),
-                  dim3(8 * kWave), stream, c, TN);
+    return launch(layer_up_kernel<F, A, CT, RC, W, WAY>, dim3((unsigned)(items < kUpGroups ? items : kUpGroups)),
+                  dim3(W * kWave), stream, c, TN);
 }
 
-template <typename F, typename A, int CT, int RCMAX, bool SHIFT>
+template <typename F, typename A, int RC, int W, Way WAY>
 hipError_t run_down(const LayerCall& c, hipStream_t stream)
 {
-    return launch(layer_down_kernel<F, A, CT, RCMAX, 8, SHIFT>, dim3((unsigned)((c.hidden + 16 * CT - 1) / (16 * CT))),
-                  dim3(8 * kWave), stream, c);
+    return launch(layer_down_kernel<F, A, RC, W, WAY>, dim3((unsigned)((c.hidden + 15) / 16)), dim3(W * kWave), stream,
+                  c);
+}
+
+// How rows of weights and of x lie: LDS takes those at 16-byte boundaries, and scales at
+// dwords'.
+template <typename F>
+Way way_of(const LayerWeights& w, const void* x, int64_t x_bytes, int64_t k)
+{
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(w.q) | reinterpret_cast<uintptr_t>(x) | (uintptr_t)x_bytes |
+                           (uintptr_t)F::row_bytes(k);
+    const uintptr_t scales = F::kBlockScales ? reinterpret_cast<uintptr_t>(w.scale) | (uintptr_t)F::row_scales(k) : 0;
+    return (rows & 15) == 0 && (scales & 3) == 0 ? Way::LDS : ((rows & 3) == 0 ? Way::ROWS : Way::SHIFTED);
+}
+
+template <typename F, typename A, int CT, int RC, int UW, int DW>
+hipError_t run_both(const LayerCall& c, hipStream_t stream)
+{
+    const Way up = way_of<F>(c.up, c.x, 2 * c.hidden, c.hidden), down = way_of<F>(c.down, nullptr, 0, c.inner);
+    const hipError_t st = up == Way::LDS    ? run_up<F, A, CT, RC, UW, Way::LDS>(c, stream)
+                          : up == Way::ROWS ? run_up<F, A, CT, RC, UW, Way::ROWS>(c, stream)
+                                            : run_up<F, A, CT, RC, UW, Way::SHIFTED>(c, stream);
+    if (st != hipSuccess)
+        return st;
+    return down == Way::LDS    ? run_down<F, A, RC, DW, Way::LDS>(c, stream)
+           : down == Way::ROWS ? run_down<F, A, RC, DW, Way::ROWS>(c, stream)
+                               : run_down<F, A, RC, DW, Way::SHIFTED>(c, stream);
 }
 
 template <typename F, typename A>
-hipError_t launch_typed(const LayerCall& c, int64_t up_bytes, int64_t down_bytes, hipStream_t stream)
+hipError_t launch_typed(const LayerCall& c, hipStream_t stream)
 {
-    const bool us = rows_shifted(c.up.q, c.x, up_bytes | (2 * c.hidden)), ds = rows_shifted(c.down.q, nullptr, down_bytes);
-    hipError_t st;
-    if (c.t <= 16)
-        st = us ? run_up<F, A, 2, 1, true>(c, stream) : run_up<F, A, 2, 1, false>(c, stream);
-    else
-        st = us ? run_up<F, A, 1, 4, true>(c, stream) : run_up<F, A, 1, 4, false>(c, stream);
-    if (st != hipSuccess)
-        return st;
-    if (c.t <= 16)
-        return ds ? run_down<F, A, 1, 1, true>(c, stream) : run_down<F, A, 1, 1, false>(c, stream);
-    return ds ? run_down<F, A, 1, 4, true>(c, stream) : run_down<F, A, 1, 4, false>(c, stream);
+    if (c.t == 1)
+        return run_both<F, A, 1, 0, 4, 8>(c, stream);
+    return c.t <= 16 ? run_both<F, A, 1, 1, 4, 8>(c, stream) : run_both<F, A, 1, 2, 4, 8>(c, stream);
 }
 
 int64_t h_pitch(int64_t inner)
@@ -503,24 +606,20 @@ int64_t h_pitch(int64_t inner)
 
 }  // namespace
 
-size_t layer_workspace_bytes(int64_t t, int64_t top, int64_t inner)
+size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t inner)
 {
-    const size_t slots = (size_t)t * (size_t)top;
-    return (slots * 8 + 15) / 16 * 16 + slots * (size_t)h_pitch(inner) * 2;
+    return (size_t)(h_rows(t, e, top) * h_pitch(inner) * 2 +
+                    4 * (2 + 3 * most_entries(t, e, top) + kPlanNumbers * t * top));
 }
 
 hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t stream)
 {
-    const size_t slots = (size_t)c.t * (size_t)c.top;
-    c.ids = static_cast<int32_t*>(ws);
-    c.weights = reinterpret_cast<float*>(c.ids + slots);
-    c.h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + (slots * 8 + 15) / 16 * 16);
     c.pitch = h_pitch(c.inner);
+    c.h = static_cast<uint16_t*>(ws);
+    c.plan = reinterpret_cast<int32_t*>(c.h + h_rows(c.t, c.e, c.top) * c.pitch);
     if (fp4)
-        return act == Act::BF16 ? launch_typed<Fp4, Bf16>(c, (c.hidden + 1) / 2, (c.inner + 1) / 2, stream)
-                                : launch_typed<Fp4, F16>(c, (c.hidden + 1) / 2, (c.inner + 1) / 2, stream);
-    return act == Act::BF16 ? launch_typed<E4m3, Bf16>(c, c.hidden, c.inner, stream)
-                            : launch_typed<E4m3, F16>(c, c.hidden, c.inner, stream);
+        return act == Act::BF16 ? launch_typed<Fp4, Bf16>(c, stream) : launch_typed<Fp4, F16>(c, stream);
+    return act == Act::BF16 ? launch_typed<E4m3, Bf16>(c, stream) : launch_typed<E4m3, F16>(c, stream);
 }
 
 }  // namespace fp8w

@@ -111,7 +111,8 @@ hipError_t launch_dequantize_fp4(const uint8_t* q, const uint8_t* scale, int64_t
                                  hipStream_t stream);
 
 constexpr int kMaxLayerTokens = 64;
-constexpr int64_t kMaxLayerWidth = (int64_t)1 << 22;  // blocks of k times experts fit an int
+constexpr int64_t kMaxLayerWidth = (int64_t)1 << 22;  // units of k times experts fit an int
+constexpr int64_t kMaxLayerValues = (int64_t)1 << 27;  // silu(gate) * up of all places, four rows for one: bytes fit an int
 
 struct LayerWeights {
     const uint8_t* q;
@@ -127,12 +128,11 @@ struct LayerCall {
     LayerWeights up, down;  // [e, 2 inner, hidden], [e, hidden, inner]
     void* out;
     // the workspace's parts, set by launch_layer
-    int32_t* ids;
-    float* weights;
     uint16_t* h;
     int64_t pitch;
+    int32_t* plan;
 };
-size_t layer_workspace_bytes(int64_t t, int64_t top, int64_t inner);
+size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t inner);
 hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t stream);
 
 // qx rows are kx >= k bytes apart (kx > k: bytes k .. kx - 1 of every row are

@@ -103,23 +103,26 @@ __device__ __forceinline__ void run_tile_staged(int S, int whole, const Load& lo
     }
 }
 
-// Stages 0 .. S - 1 (S >= NS). P: Frags; issue(s, buffer), read(buffer, half,
-// frags), mma(frags, acc). buf(integral_constant<int, i>) is stage buffer i.
-template <int NS, int LOADS, typename P, typename Buf, typename Acc>
+// Stages 0 .. S - 1 (S >= NS), each multiplied in PARTS (an even number). P: Frags;
+// issue(s, buffer), read(buffer, part, frags), mma(frags, acc). buf(integral_constant<int, i>) is stage buffer i.
+template <int NS, int LOADS, int PARTS = 2, typename P, typename Buf, typename Acc>
 __device__ __forceinline__ void run_tile_ring(const P& p, int S, const Buf& buf, Acc* acc)
 {
-    static_assert(NS >= 2 && LOADS * (NS - 1) < 64, "vmcnt range");
+    static_assert(NS >= 2 && LOADS * (NS - 1) < 64 && PARTS % 2 == 0, "vmcnt range, parts");
     typename P::Frags f0, f1;
     auto at = [&](auto i) { return buf(std::integral_constant<int, decltype(i)::value % NS>{}); };
-    // A half's reads are issued before the products of the other (scheduling barriers); behind
+    // A part's reads are issued before the products of the one before (scheduling barriers); behind
     // those the order is the compiler's, which measured 1 to 2 % faster than holding it too.
     // stage s (step u of a group of NS): `left` later stages may stay in flight
     // at the barrier (-1: this is the last stage), `more` says that stage s + NS exists
     auto step = [&](int s, auto uc, auto left, auto more) {
         constexpr int u = decltype(uc)::value;
-        p.read(at(uc), 1, f1);
-        __builtin_amdgcn_sched_barrier(0);
-        p.mma(f0, acc);
+        ring_for<1, PARTS>([&](auto h) {
+            constexpr int part = decltype(h)::value;
+            p.read(at(uc), part, part & 1 ? f1 : f0);
+            __builtin_amdgcn_sched_barrier(0);
+            p.mma(part & 1 ? f0 : f1, acc);
+        });
         if constexpr (decltype(left)::value >= 0) {
             wait_loads_at_most<LOADS * decltype(left)::value>();
             stage_barrier();

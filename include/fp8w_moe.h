@@ -223,7 +223,7 @@ typedef enum fp8w_weight_format {
  *   q_gate_up, scale_gate_up, bias_gate_up  [e, 2 inner, hidden] in `format`,
  *              bias [e, 2 inner] of act_dtype or NULL.
  *   q_down, scale_down, bias_down  [e, hidden, inner], [e, hidden].
- *   hidden, inner >= 1, up to 2^22.
+ *   hidden, inner >= 1, up to 2^22; t * top_k * (inner + 64) < 2^27.
  *   workspace of fp8w_moe_layer_workspace_bytes bytes, 16-byte aligned.
  * out and workspace must not overlap an input or each other.
  */
