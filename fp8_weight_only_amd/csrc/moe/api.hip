@@ -497,7 +497,7 @@ fp8w_status_t fp8w_linear_experts_fp4(const void* x, fp8w_dtype_t act_dtype, int
 
 size_t fp8w_moe_layer_workspace_bytes(int64_t t, int64_t e, int64_t top_k, int64_t hidden, int64_t inner)
 {
-    return layer_sizes_ok(t, e, top_k, hidden, inner) && t > 0 ? fp8w::layer_workspace_bytes(t, e, top_k, inner) : 0;
+    return layer_sizes_ok(t, e, top_k, hidden, inner) && t > 0 ? fp8w::layer_workspace_bytes(t, e, top_k, hidden, inner) : 0;
 }
 
 fp8w_status_t fp8w_moe_layer(const void* x, fp8w_dtype_t act_dtype, int64_t t, int64_t hidden, const void* logits,
@@ -518,7 +518,7 @@ fp8w_status_t fp8w_moe_layer(const void* x, fp8w_dtype_t act_dtype, int64_t t, i
     if (!aligned(x, 2) || !aligned(logits, elem_bytes(logits_dtype)) || !aligned(scale_gate_up, scale_align) ||
         !aligned(bias_gate_up, 2) || !aligned(scale_down, scale_align) || !aligned(bias_down, 2) || !aligned(out, 2))
         return FP8W_ERR_MISALIGNED;
-    const size_t need = fp8w::layer_workspace_bytes(t, e, top_k, inner), tokens = (size_t)t * (size_t)hidden * 2;
+    const size_t need = fp8w::layer_workspace_bytes(t, e, top_k, hidden, inner), tokens = (size_t)t * (size_t)hidden * 2;
     if (!workspace || workspace_bytes < need)
         return FP8W_ERR_WORKSPACE;
     if (!aligned(workspace, 16))

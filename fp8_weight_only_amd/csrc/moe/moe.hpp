@@ -131,8 +131,10 @@ struct LayerCall {
     uint16_t* h;
     int64_t pitch;
     int32_t* plan;
+    uint32_t* arrived;  // per 16 output channels
+    float* parts;
 };
-size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t inner);
+size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t hidden, int64_t inner);
 hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t stream);
 
 // qx rows are kx >= k bytes apart (kx > k: bytes k .. kx - 1 of every row are

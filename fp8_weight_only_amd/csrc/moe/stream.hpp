@@ -71,32 +71,6 @@ struct Buffer {
     __device__ __forceinline__ int at(bool on, int off) const { return on ? off : bytes; }
 };
 
-// 16 bytes of a row from any byte on (SHIFT), else from a dword: device.hpp, Row.
-template <bool SHIFT>
-struct Piece {
-    u32x4 v;
-    uint32_t e[SHIFT ? 1 : 0], shift[SHIFT ? 1 : 0];
-
-    __device__ __forceinline__ void load(const Buffer& b, int off, int scalar_off)
-    {
-        if constexpr (SHIFT) {
-            off += b.rest;
-            shift[0] = (uint32_t)off & 3u;
-            off -= (int)shift[0];
-            e[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(b.rsrc, off + (shift[0] ? 16 : 0), scalar_off, 0);
-        }
-        v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.rsrc, off, scalar_off, 0));
-    }
-    __device__ __forceinline__ u32x4 bytes() const
-    {
-        const u32x4 d = v;
-        if constexpr (SHIFT)
-            return u32x4{__builtin_amdgcn_alignbyte(d.y, d.x, shift[0]), __builtin_amdgcn_alignbyte(d.z, d.y, shift[0]),
-                         __builtin_amdgcn_alignbyte(d.w, d.z, shift[0]), __builtin_amdgcn_alignbyte(e[0], d.w, shift[0])};
-        return d;
-    }
-};
-
 // The first n bytes of 16 (n <= 0: none).
 __device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n)
 {
@@ -116,6 +90,12 @@ __device__ __forceinline__ u32x4 E4m3::first(u32x4 v, int n)
 
 // NT tiles of 16 weight rows, in NB buffers of as many each, times RC tiles of 16
 // activation rows, from any byte on (SHIFT), else from dwords. lane % 16 is a lane's row.
+//
+// Rows at any byte come as the dwords that hold them, put together by byte shifts. The dword
+// behind a lane's 16 bytes is the first of the lane's that has the next 16, and only the
+// step's last is loaded by itself: a load of a dword costs the address unit as much as one of 16 bytes
+// (13 tokens over 60 e4m3 experts of [1026, 1030] and [1030, 513]: 17.8 and 25.8 us, with a load each
+// 20.1 and 28.0).
 //
 // X4: x is kept in groups of four rows, eight values of each in turn, as the layer's
 // second launch reads what its first wrote: a quad's lanes then read 64 consecutive
@@ -140,8 +120,9 @@ struct RowStream {
         int xoff[RC];
         bool xon[RC];  // some row of this tile is wanted
     };
-    Piece<SHIFT> w[NT][U];
-    Piece<SHIFT && !X4> xs[RC][U][P];
+    static constexpr bool XSHIFT = SHIFT && !X4;
+    u32x4 w[NT][U], xs[RC][U][P];
+    uint32_t wshift[SHIFT ? NT : 0], wlast[SHIFT ? NT : 0], xshift[XSHIFT ? RC : 0], xlast[XSHIFT ? RC : 0];
     uint8_t s[F::kBlockScales ? NT : 0][U];
 
     __device__ __forceinline__ RowStream(int64_t k_, const void* x_, int64_t x_bytes, uint8_t*) : k(k_), x(x_, x_bytes)
@@ -188,18 +169,61 @@ struct RowStream {
                     s[t][h] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(of.rsrc, soff[t % TILES] + of.rest + 4 * h,
                                                                            of.at(on, 4 * U * step), 0);
                 }
+        auto load16 = [](const Buffer& from, int off, int scalar_off) {
+            return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from.rsrc, off, scalar_off, 0));
+        };
 #pragma unroll
-        for (int h = 0; h < U; ++h) {
+        for (int t = 0; t < NT; ++t) {
+            const Buffer& from = src.w[t / TILES];
+            int off = woff[t % TILES];
+            const int at = from.at(on, 64 * U * step);
+            if constexpr (SHIFT) {
+                off += from.rest;
+                wshift[t] = (uint32_t)off & 3u;
+                off -= (int)wshift[t];
+                wlast[t] = 0;
+                if (g == 3)
+                    wlast[t] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(from.rsrc, off + 64 * (U - 1) + 16, at, 0);
+            }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                w[t][h].load(src.w[t / TILES], woff[t % TILES] + 64 * h, src.w[t / TILES].at(on, 64 * U * step));
+            for (int h = 0; h < U; ++h)
+                w[t][h] = load16(from, off + 64 * h, at);
+        }
 #pragma unroll
-            for (int u = 0; u < RC; ++u)
+        for (int u = 0; u < RC; ++u) {
+            int off = src.xoff[u];
+            const int at = x.at(on && src.xon[u], BY * K * step);
+            if constexpr (XSHIFT) {
+                off += x.rest;
+                xshift[u] = (uint32_t)off & 3u;
+                off -= (int)xshift[u];
+                xlast[u] = 0;
+                if (g == 3)
+                    xlast[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                        x.rsrc, off + BY * F::kUnit * (U - 1) + 16 * P, at, 0);
+            }
+#pragma unroll
+            for (int h = 0; h < U; ++h)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    xs[u][h][p].load(x, src.xoff[u] + BY * (F::kUnit * h + 8 * p),
-                                     x.at(on && src.xon[u], BY * K * step));
+                    xs[u][h][p] = load16(x, off + BY * (F::kUnit * h + 8 * p), at);
         }
+    }
+    // The dword behind each unit's bytes of this lane: first[h] is the unit's first, last the one behind the step.
+    __device__ __forceinline__ void behind(const uint32_t (&first)[U], uint32_t last, uint32_t (&e)[U]) const
+    {
+        const int from = 4 * ((int)(threadIdx.x + 16) & 63);
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+            const uint32_t give = g == 0 && h + 1 < U ? first[h + 1 < U ? h + 1 : h] : first[h];
+            const uint32_t got = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)give);
+            e[h] = g == 3 && h + 1 == U ? last : got;
+        }
+    }
+    __device__ __forceinline__ static u32x4 shifted(u32x4 v, uint32_t e, uint32_t by)
+    {
+        return u32x4{__builtin_amdgcn_alignbyte(v.y, v.x, by), __builtin_amdgcn_alignbyte(v.z, v.y, by),
+                     __builtin_amdgcn_alignbyte(v.w, v.z, by), __builtin_amdgcn_alignbyte(e, v.w, by)};
     }
     // Adds the loaded step's products, step `step` of k, and loads step `next` of src.
     __device__ __forceinline__ void consume(int step, const Source& src, int next, bool on, f32x4 (&acc)[NT][RC])
@@ -210,7 +234,7 @@ struct RowStream {
         for (int h = 0; h < U; ++h) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                v[t][h] = w[t][h].bytes();
+                v[t][h] = w[t][h];
                 scale[t][h] = 1.0f;
                 if constexpr (F::kBlockScales)
                     scale[t][h] = fp4_scale(s[t][h]);
@@ -219,8 +243,36 @@ struct RowStream {
             for (int u = 0; u < RC; ++u)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    xv[u][h][p] = xs[u][h][p].bytes();
+                    xv[u][h][p] = xs[u][h][p];
         }
+        if constexpr (SHIFT)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                uint32_t first[U], e[U];
+#pragma unroll
+                for (int h = 0; h < U; ++h)
+                    first[h] = v[t][h].x;
+                behind(first, wlast[t], e);
+#pragma unroll
+                for (int h = 0; h < U; ++h)
+                    v[t][h] = shifted(v[t][h], e[h], wshift[t]);
+            }
+        if constexpr (XSHIFT)
+#pragma unroll
+            for (int u = 0; u < RC; ++u) {
+                uint32_t first[U], e[U];
+#pragma unroll
+                for (int h = 0; h < U; ++h)
+                    first[h] = xv[u][h][0].x;
+                behind(first, xlast[u], e);
+#pragma unroll
+                for (int h = 0; h < U; ++h)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        const uint32_t next_dword = p + 1 < P ? xv[u][h][p + 1 < P ? p + 1 : p].x : e[h];
+                        xv[u][h][p] = shifted(xv[u][h][p], next_dword, xshift[u]);
+                    }
+            }
         load(src, next, on);
         if ((int64_t)K * (step + 1) > k) {  // what lies behind a row's end is the next row's
 #pragma unroll
