@@ -849,11 +849,14 @@ const char* fp4_kernel_name(const Fp4Shape& s, const void* x, const uint8_t* q, 
 {
     thread_local char name[96];
     const Fp4Plan p = fp4_plan(s, x, q, scale);
+    char join[32] = "";
+    if (p.slices > 1)
+        snprintf(join, sizeof join, "*%d+fp4_join_kernel", p.slices);
     if (p.kind == Fp4Kind::STREAM)
         snprintf(name, sizeof name, "fp4_stream_kernel<CT=%d,WK=%d,WC=%d>", p.a, p.w, p.c);
     else
-        snprintf(name, sizeof name, "fp4_%s_kernel<BN=%d,BM=%d,W=%d>,slices=%d", p.kind == Fp4Kind::TILE ? "tile" : "ring",
-                 p.a, p.b, p.w, p.slices);
+        snprintf(name, sizeof name, "fp4_%s_kernel<BN=%d,BM=%d,W=%d>%s", p.kind == Fp4Kind::TILE ? "tile" : "ring", p.a,
+                 p.b, p.w, join);
     return name;
 }
 
