@@ -208,6 +208,9 @@ __device__ __forceinline__ int token_of_row(uint64_t tokens)
 //
 // RC: tiles of 16 rows (0: one token, whose choices every wave makes for itself, with
 // no barrier before the first loads).
+//
+// One token, two of eight e4m3 experts [28672, 4096]: 47 us, 5.0 TB/s. 64 tokens over all eight: 234 us,
+// the address unit busy 80 % with the activations. 16 tokens over 128 4-bit experts [2048, 4096]: 88.
 template <typename F, typename A, int CT, int RC, int W, Way WAY>
 __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int TN)
 {
@@ -428,7 +431,8 @@ __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int 
 
 // A workgroup has 16 output channels of every token. A wave's steps run over the active
 // experts; at an expert's end (or the wave's own) its sums go to the wave's accumulators
-// of the tokens.
+// of the tokens. One token, two of eight e4m3 experts [4096, 14336]: 25.5 us, 4.6 TB/s; 64 tokens
+// over all eight: 122.
 //
 // Where there are few channels the steps are shared by `slices` workgroups: each leaves its
 // sums in the workspace and counts itself in (the first launch cleared the counts), and the last
