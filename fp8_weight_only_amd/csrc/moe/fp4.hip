@@ -39,8 +39,8 @@ __device__ __forceinline__ RowTile row_tile(const Fp4Call& c, int want)
 // every WK-th step of k; the sums of WK waves meet in LDS and are added in wave order.
 // A wave's loads run a step ahead, into the next tile's weights.
 //
-// One row, [14336, 4096]: 9.2 us, 3.4 TB/s of a 5.1 floor rate; eight steps a wave leave start and drain
-// uncovered ([28672, 8192]: 29.7 us, 4.2 TB/s). 512 rows over 128 experts [4096, 1024]: 61 us, 3.8
+// One row, [14336, 4096]: 9.2 us, 3.4 TB/s, as a wave's eight steps leave start and drain uncovered
+// ([28672, 8192]: 29.7 us, 4.2 TB/s). 512 rows over 128 experts [4096, 1024]: 61 us, 3.8
 // TB/s, the address unit busy 68 %.
 template <typename A, int CT, int WK, int WC, Way WAY>
 __global__ __launch_bounds__(WK* WC* kWave) void fp4_stream_kernel(Fp4Call c, int TN, int cols)

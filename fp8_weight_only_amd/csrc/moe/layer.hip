@@ -7,10 +7,10 @@
 //
 // First launch: every workgroup chooses for all tokens rather than wait for a launch
 // that does. Its items are 16 CT channels of one active expert, gate and up rows
-// together, with all the expert's rows (up to 64), so every weight is read once. The
+// together, with up to 32 of its rows: an expert with more is read twice. The
 // first workgroup leaves the plan for the second launch.
 //
-// Second launch: a workgroup owns 16 CT output channels of every token. The active
+// Second launch: a workgroup owns 16 output channels of every token. The active
 // experts' blocks of k, in one line, are split evenly over its waves; a wave adds
 // weights[t, j] times its part of an expert's sums to its own fp32 accumulators in
 // LDS, and the waves' accumulators are added in wave order. No slot's result goes
@@ -210,7 +210,7 @@ __device__ __forceinline__ int token_of_row(uint64_t tokens)
 // no barrier before the first loads).
 //
 // One token, two of eight e4m3 experts [28672, 4096]: 47 us, 5.0 TB/s. 64 tokens over all eight: 234 us,
-// the address unit busy 80 % with the activations. 16 tokens over 128 4-bit experts [2048, 4096]: 88.
+// the address unit busy 80 % (two tiles of channels, half the activations' loads: 233). 16 tokens over 128 4-bit experts [2048, 4096]: 88.
 template <typename F, typename A, int CT, int RC, int W, Way WAY>
 __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int TN)
 {
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int 
     __shared__ __attribute__((aligned(16))) float part[W][2 * CT][4 * kWave];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const Plan plan = plan_of(c);
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0 && c.arrived)
         for (int i = tid; i < (int)output_tiles(c.hidden); i += NT)
             c.arrived[i] = 0;
     int count, one_id = -1;
@@ -675,7 +675,7 @@ size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t hidden, 
 {
     return (size_t)(h_rows(t, e, top) * h_pitch(inner) * 2 +
                     4 * (plan_numbers(t, e, top) +
-                         output_tiles(hidden) * (1 + (most_slices(hidden) > 1 ? most_slices(hidden) * t * 16 : 0))));
+                         (most_slices(hidden) > 1 ? output_tiles(hidden) * (1 + most_slices(hidden) * t * 16) : 0)));
 }
 
 hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t stream)
@@ -683,8 +683,12 @@ hipError_t launch_layer(LayerCall c, bool fp4, Act act, void* ws, hipStream_t st
     c.pitch = h_pitch(c.inner);
     c.h = static_cast<uint16_t*>(ws);
     c.plan = reinterpret_cast<int32_t*>(c.h + h_rows(c.t, c.e, c.top) * c.pitch);
-    c.arrived = reinterpret_cast<uint32_t*>(c.plan + plan_numbers(c.t, c.e, c.top));
-    c.parts = reinterpret_cast<float*>(c.arrived + output_tiles(c.hidden));
+    c.arrived = nullptr;
+    c.parts = nullptr;
+    if (most_slices(c.hidden) > 1) {
+        c.arrived = reinterpret_cast<uint32_t*>(c.plan + plan_numbers(c.t, c.e, c.top));
+        c.parts = reinterpret_cast<float*>(c.arrived + output_tiles(c.hidden));
+    }
     if (fp4)
         return act == Act::BF16 ? launch_typed<Fp4, Bf16>(c, stream) : launch_typed<Fp4, F16>(c, stream);
     return act == Act::BF16 ? launch_typed<E4m3, Bf16>(c, stream) : launch_typed<E4m3, F16>(c, stream);

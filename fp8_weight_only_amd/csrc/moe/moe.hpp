@@ -131,7 +131,7 @@ struct LayerCall {
     uint16_t* h;
     int64_t pitch;
     int32_t* plan;
-    uint32_t* arrived;  // per 16 output channels
+    uint32_t* arrived;  // per 16 output channels, null where one workgroup has them
     float* parts;
 };
 size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t top, int64_t hidden, int64_t inner);
