@@ -19,6 +19,7 @@
 
 #include "../ring.hpp"
 #include "fp4.hpp"
+#include "offset.hpp"
 
 namespace fp8w {
 
@@ -52,7 +53,8 @@ struct Fp4 {
 };
 
 // A buffer for loads that are the same in all lanes but for a 32-bit offset: reads
-// past its end give zeros and touch no memory (each dword for itself, measured too).
+// past its end give zeros and touch no memory (each dword for itself, measured too),
+// as long as their scalar offset is not past it (offset.hpp).
 struct Buffer {
     __amdgpu_buffer_rsrc_t rsrc;  // from the dword boundary at or before the data
     int bytes, rest;              // the data start `rest` behind it
@@ -67,8 +69,12 @@ struct Buffer {
         bytes = all < 0x70000000 ? (int)all : 0x70000000;  // offsets past it stay ints
         rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at - rest), 0, bytes, 0x00020000);
     }
-    // the scalar offset of a load, past the end when it is not on
-    __device__ __forceinline__ int at(bool on, int off) const { return on ? off : bytes; }
+    // the scalar offset of a load: the end when it is not on
+    __device__ __forceinline__ int at(bool on, int off) const { return buffer_offset(on, off, bytes); }
+    __device__ __forceinline__ int at(bool on, int off, int row, int row_bytes) const
+    {
+        return buffer_offset(on, off, row, row_bytes, bytes);
+    }
 };
 
 // The first n bytes of 16 (n <= 0: none).
@@ -371,13 +377,13 @@ struct LdsStream {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const Buffer& from = src.w[t / TILES];
-            const int at = from.at(on, 256 * step) + 16 * (t % TILES) * row_bytes;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 // lane: row 4 q + g, place r
                 const int chunk = 4 * ((r / 4 - g) & 3) + ((r ^ q) & 3);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(from.rsrc, FP8W_LDS(lds + 4096 * t + 1024 * q), 16,
-                                                         woff + 16 * chunk, at + 4 * q * row_bytes, 0, 0);
+                                                         woff + 16 * chunk,
+                                                         from.at(on, 256 * step, 16 * (t % TILES) + 4 * q, row_bytes), 0, 0);
             }
         }
         if constexpr (F::kBlockScales)
@@ -385,7 +391,7 @@ struct LdsStream {
             for (int t = 0; t < NT; ++t) {
                 const Buffer& of = src.s[t / TILES];
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(of.rsrc, FP8W_LDS(lds + WBYTES + 256 * t), 4, soff,
-                                                         of.at(on, 16 * step) + 16 * (t % TILES) * row_scales, 0, 0);
+                                                         of.at(on, 16 * step, 16 * (t % TILES), row_scales), 0, 0);
             }
         asm volatile("" ::: "memory");
     }
