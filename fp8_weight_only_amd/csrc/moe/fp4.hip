@@ -322,7 +322,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_tile_kernel(Fp4Call c, int 
 }
 
 // Rows at 16-byte boundaries, k a multiple of 64 Q (and of 128), scales at dword
-// boundaries, x below 2 GiB: the same tiles fed by a ring of NS direct-to-LDS stages
+// boundaries, experts' x below 2 GiB: the same tiles fed by a ring of NS direct-to-LDS stages
 // (tile.hpp) of 64 Q k. Scales come as dwords of 128 k: a stage of 64 k uses half of
 // it, the lower pair in an even stage, the upper in an odd one.
 template <int I>
@@ -486,7 +486,10 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
         const int64_t first = (int64_t)tile.expert * c.n + n0;
         p.w = Rows(c.q + first * c.row_bytes);
         p.sc = Rows(c.block_scale + first * c.row_scales);
-        p.x = Rows(c.x);
+        // the linear layer's rows are offset from the tile's first, so that x may be of any size (past 2 GiB
+        // only the stream was left: 74899 tokens [4096, 14336] 36.9 ms, 74898 and now both 7.8)
+        const int64_t from = c.offsets ? 0 : tile.row * c.k;
+        p.x = Rows(static_cast<const uint16_t*>(c.x) + from);
         auto row = [&](int r) { return (int)(n0 + r < c.n ? r : c.n - 1 - n0); };
 #pragma unroll
         for (int u = 0; u < P::LW; ++u) {
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
 #pragma unroll
         for (int u = 0; u < P::LX; ++u) {
             const int piece = u * T::W + p.wave, r = 8 * (piece % (BM / 8)) + (p.lane >> 3);
-            p.off[P::LW + u] = (int)(2 * source_row(c, tile, r) * c.k) + 128 * (piece / (BM / 8)) +
+            p.off[P::LW + u] = (int)(2 * (source_row(c, tile, r) * c.k - from)) + 128 * (piece / (BM / 8)) +
                                16 * (((p.lane & 7) - (r >> 1)) & 7);
         }
 #pragma unroll
@@ -731,7 +734,7 @@ Fp4Plan fp4_plan(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8
     // Few rows to an expert: rings of 32 rows load and multiply mostly nothing (128 experts of
     // [4096, 1024], four rows each: 91 us, the stream 62).
     const bool few = s.grouped && rows <= 16 && any;
-    if (aligned && !few && s.k > 0 && s.k <= (1 << 22) && s.xr <= ((int64_t)1 << 30) / s.k) {
+    if (aligned && !few && s.k > 0 && s.k <= (1 << 22) && (!s.grouped || s.xr <= ((int64_t)1 << 30) / s.k)) {
         for (const Fp4Plan& p : kRings)
             for (int z = 1; z <= (s.grouped ? 1 : 16); z *= 2) {
                 Fp4Plan v = p;
