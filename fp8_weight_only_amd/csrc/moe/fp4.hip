@@ -711,6 +711,14 @@ bool stream_fits(const Fp4Shape& s, const Fp4Plan& p)
     return p.fits(s) && s.k <= (1 << 22) && rows * s.k < (1 << 29);
 }
 
+// Whether some row starts below dword alignment.
+bool rows_shifted(const void* x, const uint8_t* q, int64_t k)
+{
+    return ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(q) | (uintptr_t)(2 * k) |
+             (uintptr_t)Fp4::row_bytes(k)) &
+            3) != 0;
+}
+
 // aligned: rows and scales as the ring and the stream's LDS way take them.
 Fp4Plan fp4_plan(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8_t* scale)
 {
@@ -750,7 +758,16 @@ Fp4Plan fp4_plan(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8
     for (const Fp4Plan& p : kTiles)
         if (p.b <= bm && (s.n + p.a - 1) / p.a * active * ((rows + p.b - 1) / p.b) >= 224 && p.fits(s))
             return p;
-    return kTiles[2];
+    // Few tiles, which walk a long k on a part of the CUs: a stream that is modelled a quarter faster (of rows at
+    // any byte it takes up to 1.3 times its model) than the one round of 64 x 64 tiles takes. Measured, us:
+    // [4096, 14330] with 17, 64, 128 tokens 33, 48, 88, tiles 110, 139, 131; [1024, 8128] with 17, 200 tokens
+    // 11.8, 23, tiles 37, 37; two experts [4096, 14330], 20 rows each, 45, tiles 113; eight [512, 4090], 64 rows
+    // each, 17, tiles 34. From 224 tiles on they are even or slower: [4096, 14330] with 200 tokens 158, tiles 108.
+    const double tile_us = 3.0 + (double)s.k / 64.0 * (rows_shifted(x, q, s.k) ? 0.47 : 0.34);
+    for (const Fp4Plan& p : kStreams)
+        if (stream_fits(s, p))
+            offer(p);
+    return any && low < 0.75 * tile_us ? found : kTiles[2];
 }
 
 Fp4Shape shape_of(const Fp4Call& c)
@@ -758,12 +775,9 @@ Fp4Shape shape_of(const Fp4Call& c)
     return {c.m, c.e, c.n, c.k, c.xr, c.offsets != nullptr};
 }
 
-// Whether some row starts below dword alignment.
 bool shifted(const Fp4Call& c)
 {
-    return ((reinterpret_cast<uintptr_t>(c.x) | reinterpret_cast<uintptr_t>(c.q) | (uintptr_t)(2 * c.k) |
-             (uintptr_t)c.row_bytes) &
-            3) != 0;
+    return rows_shifted(c.x, c.q, c.k);
 }
 
 // LDS takes rows at 16-byte boundaries, and scales at dwords, in steps of four units: where
