@@ -11,7 +11,7 @@
 
 namespace fp8w {
 
-template <typename A, bool SCALED = true>
+template <typename A>
 __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos, int expert, int64_t c0, int count,
                                                const float* acc)
 {
@@ -36,8 +36,8 @@ __device__ __forceinline__ void store_tile_row(const ExpertCall& c, int64_t pos,
             continue;
         }
         const int64_t ch = (int64_t)expert * c.n + c0 + r;
-        const float scale = SCALED ? c.scale[ch] : 1.0f;
-        o[r] = rounded<A>(__builtin_fmaf(scale, ok ? acc[r] : __builtin_nanf(""), A::to_f32(bias_bits(bias, ch))));
+        o[r] = rounded<A>(
+            __builtin_fmaf(c.scale[ch], ok ? acc[r] : __builtin_nanf(""), A::to_f32(bias_bits(bias, ch))));
     }
     store4(out, o, count);
 }

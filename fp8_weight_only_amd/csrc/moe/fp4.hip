@@ -444,22 +444,15 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
 {
     using P = Fp4Ring<A, BN, BM, WN, WM, NS, Q>;
     using T = Fp4Tile<A, BN, BM, WN, WM, Q>;
-    static_assert(NS >= 2 && NS <= 8, "stages");
+    static_assert(NS >= 2 && NS <= 4, "stages");
     __shared__ __attribute__((aligned(1024))) uint8_t b0[P::STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t b1[P::STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t b2[NS > 2 ? P::STAGE : 16];
     __shared__ __attribute__((aligned(1024))) uint8_t b3[NS > 3 ? P::STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b4[NS > 4 ? P::STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b5[NS > 5 ? P::STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b6[NS > 6 ? P::STAGE : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t b7[NS > 7 ? P::STAGE : 16];
     __shared__ __attribute__((aligned(16))) ExpertEpilogue<BN, BM> epi;
     auto buf = [&](auto ic) {
         constexpr int i = decltype(ic)::value;
-        if constexpr (i < 4)
-            return RingSlot<i>{ring_buf<i>(b0, b1, b2, b3)};
-        else
-            return RingSlot<i>{ring_buf<i - 4>(b4, b5, b6, b7)};
+        return RingSlot<i>{ring_buf<i>(b0, b1, b2, b3)};
     };
     int tn;
     RowTile tile;
@@ -520,7 +513,6 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
         store_sums<BN, BM, WN, WM>(c, p, c.parts + slice * c.m * parts_row(c.n), tile, n0, acc);
         return;
     }
-    __syncthreads();
     store_tile<A, BN, BM, WN, WM>(c, p, n0, epi, acc);
 }
 

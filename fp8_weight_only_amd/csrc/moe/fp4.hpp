@@ -12,8 +12,6 @@
 
 namespace fp8w {
 
-constexpr int kFp4Block = 32;
-
 // The scale operand of the conversion for an e8m0 byte (255: NaN).
 __device__ __forceinline__ float fp4_scale(uint32_t byte)
 {

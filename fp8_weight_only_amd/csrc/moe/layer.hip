@@ -6,7 +6,7 @@
 // with a scale per output channel, or 4-bit codes with block scales (fp4.hpp).
 //
 // First launch: every workgroup chooses for all tokens rather than wait for a launch
-// that does. Its items are 16 CT channels of one active expert, gate and up rows
+// that does. Its items are 16 channels of one active expert, gate and up rows
 // together, with up to 32 of its rows: an expert with more is read twice. The
 // first workgroup leaves the plan for the second launch.
 //
@@ -201,7 +201,7 @@ __device__ __forceinline__ int token_of_row(uint64_t tokens)
     return __builtin_amdgcn_ds_permute(4 * to, lane);  // a permutation: every lane is written once
 }
 
-// An item is 16 CT channels of gate and of up of one active expert; a workgroup has
+// An item is 16 channels of gate and of up of one active expert; a workgroup has
 // every gridDim.x-th. Its W waves take the steps of k in turn. A wave's loads run a step
 // ahead, into the next item while this one's sums meet in LDS, so the stream of weights
 // does not stop between items.
@@ -211,19 +211,18 @@ __device__ __forceinline__ int token_of_row(uint64_t tokens)
 //
 // One token, two of eight e4m3 experts [28672, 4096]: 47 us, 5.0 TB/s. 64 tokens over all eight: 234 us,
 // the address unit busy 80 % (two tiles of channels, half the activations' loads: 233). 16 tokens over 128 4-bit experts [2048, 4096]: 88.
-template <typename F, typename A, int CT, int RC, int W, Way WAY>
+template <typename F, typename A, int RC, int W, Way WAY>
 __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int TN)
 {
-    constexpr int NT = W * kWave, CH = 16 * CT, RT = RC == 0 ? 1 : RC;
-    static_assert(NT % CH == 0, "a thread's values are of one channel");
+    constexpr int NT = W * kWave, CH = 16, RT = RC == 0 ? 1 : RC;  // a thread's values are of one channel
     constexpr bool ONE = RC == 0;
     constexpr int SLOTS = (RC <= 1 ? 16 : kMaxLayerTokens) * kMaxTop;
-    using S = Stream<F, A, 2 * CT, 2, RT, WAY, false>;
+    using S = Stream<F, A, 2, 2, RT, WAY, false>;  // gate, up
     using C = Choices<SLOTS>;
     constexpr size_t kRing = (size_t)W * S::LDS, kChoices = ONE ? 16 : sizeof(C);
     __shared__ std::conditional_t<ONE, char, Lists> lists;
     __shared__ __attribute__((aligned(16))) uint8_t ring[kRing > kChoices ? kRing : kChoices];
-    __shared__ __attribute__((aligned(16))) float part[W][2 * CT][4 * kWave];
+    __shared__ __attribute__((aligned(16))) float part[W][2][4 * kWave];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const Plan plan = plan_of(c);
     if (blockIdx.x == 0 && c.arrived)
@@ -374,9 +373,9 @@ __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int 
         const float* scale = static_cast<const float*>(c.up.scale);
         const float gs = F::kBlockScales ? 1.0f : scale[gc], us = F::kBlockScales ? 1.0f : scale[uc];
         const uint16_t gb = bias_bits(bias, gc), ub = bias_bits(bias, uc);
-        f32x4 acc[2 * CT][RT];
+        f32x4 acc[2][RT];
 #pragma unroll
-        for (int t = 0; t < 2 * CT; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int u = 0; u < RT; ++u)
                 acc[t][u] = f32x4{0.0f};
@@ -398,7 +397,7 @@ __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int 
             if (16 * u >= item.rows)
                 break;
 #pragma unroll
-            for (int t = 0; t < 2 * CT; ++t) {
+            for (int t = 0; t < 2; ++t) {
                 f32x4 sums = acc[t][0];
 #pragma unroll
                 for (int q = 1; q < RT; ++q)
@@ -410,12 +409,12 @@ __global__ __launch_bounds__(W* kWave, 2) void layer_up_kernel(LayerCall c, int 
             const int here = item.rows - 16 * u < 16 ? item.rows - 16 * u : 16;
 #pragma unroll 1
             for (int row = tid / CH; row < here; row += NT / CH) {
-                const int at = 4 * (row + 16 * ((ch & 15) >> 2)) + (ch & 3);
+                const int at = 4 * (row + 16 * (ch >> 2)) + (ch & 3);
                 float gate = 0.0f, lift = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    gate += part[w][ch / 16][at];
-                    lift += part[w][CT + ch / 16][at];
+                    gate += part[w][0][at];
+                    lift += part[w][1][at];
                 }
                 gate = __builtin_fmaf(gs, gate, A::to_f32(gb));
                 lift = __builtin_fmaf(us, lift, A::to_f32(ub));
@@ -525,38 +524,38 @@ __global__ __launch_bounds__(W* kWave) void layer_down_kernel(LayerCall c, int s
         acc[0][u] = f32x4{0.0f};
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-            const bool more = i + 1 < n;
-            if (++lp == per && more) {
-                lp = 0;
-                enter(++la);
-            }
-            const u32x4 scale_next = load_scale(more && (lp + 1 == per || i + 2 == n));
-            st.consume(cp, src, lp, more, acc);
-            if (++cp == per || !more) {
-                const int first = uniform(start[ca]), rows = uniform(start[ca + 1]) - first;
-                const f32x4 scale = F::kBlockScales ? f32x4{1.0f, 1.0f, 1.0f, 1.0f} : __builtin_bit_cast(f32x4, scale_bits);
-                // lane (r, g): channels 4 g .. 4 g + 3 of row r; an expert has a token once
+        const bool more = i + 1 < n;
+        if (++lp == per && more) {
+            lp = 0;
+            enter(++la);
+        }
+        const u32x4 scale_next = load_scale(more && (lp + 1 == per || i + 2 == n));
+        st.consume(cp, src, lp, more, acc);
+        if (++cp == per || !more) {
+            const int first = uniform(start[ca]), rows = uniform(start[ca + 1]) - first;
+            const f32x4 scale = F::kBlockScales ? f32x4{1.0f, 1.0f, 1.0f, 1.0f} : __builtin_bit_cast(f32x4, scale_bits);
+            // lane (r, g): channels 4 g .. 4 g + 3 of row r; an expert has a token once
 #pragma unroll
-                for (int u = 0; u < RT; ++u) {
-                    if (16 * u + r < rows) {
-                        const int row = first + 16 * u + r;
-                        f32x4& to = sum[wave][TOKENS == 1 ? 0 : token[row]][g];
-                        const f32x4 v = acc[0][u];
-                        const float w = weight[row];
-                        f32x4 z = to;
-                        z.x = __builtin_fmaf(w, scale.x * v.x, z.x);
-                        z.y = __builtin_fmaf(w, scale.y * v.y, z.y);
-                        z.z = __builtin_fmaf(w, scale.z * v.z, z.z);
-                        z.w = __builtin_fmaf(w, scale.w * v.w, z.w);
-                        to = z;
-                    }
-                    acc[0][u] = f32x4{0.0f};
+            for (int u = 0; u < RT; ++u) {
+                if (16 * u + r < rows) {
+                    const int row = first + 16 * u + r;
+                    f32x4& to = sum[wave][TOKENS == 1 ? 0 : token[row]][g];
+                    const f32x4 v = acc[0][u];
+                    const float w = weight[row];
+                    f32x4 z = to;
+                    z.x = __builtin_fmaf(w, scale.x * v.x, z.x);
+                    z.y = __builtin_fmaf(w, scale.y * v.y, z.y);
+                    z.z = __builtin_fmaf(w, scale.z * v.z, z.z);
+                    z.w = __builtin_fmaf(w, scale.w * v.w, z.w);
+                    to = z;
                 }
-                wave_sync();
-                cp = 0;
-                ++ca;
+                acc[0][u] = f32x4{0.0f};
             }
-            scale_bits = scale_next;
+            wave_sync();
+            cp = 0;
+            ++ca;
+        }
+        scale_bits = scale_next;
     }
     __syncthreads();
 #pragma unroll 1
@@ -597,7 +596,7 @@ __global__ __launch_bounds__(W* kWave) void layer_down_kernel(LayerCall c, int s
 }
 
 // ------------------------------------------------------------------ plans
-constexpr int kUpGroups = 1024;
+constexpr int kUpGroups = 1024, kUpWaves = 4, kDownWaves = 8;
 
 // Workgroups to the second launch's 16 channels: one where those alone take most CUs, else up to
 // as many as there are CUs for.
@@ -607,12 +606,12 @@ int64_t most_slices(int64_t hidden)
     return tiles > 160 ? 1 : std::min<int64_t>(8, (256 + tiles - 1) / tiles);
 }
 
-template <typename F, typename A, int CT, int RC, int W, Way WAY>
+template <typename F, typename A, int RC, int W, Way WAY>
 hipError_t run_up(const LayerCall& c, hipStream_t stream)
 {
-    const int64_t TN = (c.inner + 16 * CT - 1) / (16 * CT), most = most_entries(c.t, c.e, c.top);
+    const int64_t TN = (c.inner + 15) / 16, most = most_entries(c.t, c.e, c.top);
     const int64_t items = TN * most;
-    return launch(layer_up_kernel<F, A, CT, RC, W, WAY>, dim3((unsigned)(items < kUpGroups ? items : kUpGroups)),
+    return launch(layer_up_kernel<F, A, RC, W, WAY>, dim3((unsigned)(items < kUpGroups ? items : kUpGroups)),
                   dim3(W * kWave), stream, c, TN);
 }
 
@@ -637,26 +636,26 @@ Way way_of(const LayerWeights& w, const void* x, int64_t x_bytes, int64_t k)
     return (rows & 15) == 0 && (scales & 3) == 0 ? Way::LDS : ((rows & 3) == 0 ? Way::ROWS : Way::SHIFTED);
 }
 
-template <typename F, typename A, int CT, int RC, int UW, int DW>
+template <typename F, typename A, int RC>
 hipError_t run_both(const LayerCall& c, hipStream_t stream)
 {
     const Way up = way_of<F>(c.up, c.x, 2 * c.hidden, c.hidden), down = way_of<F>(c.down, nullptr, 0, c.inner);
-    const hipError_t st = up == Way::LDS    ? run_up<F, A, CT, RC, UW, Way::LDS>(c, stream)
-                          : up == Way::ROWS ? run_up<F, A, CT, RC, UW, Way::ROWS>(c, stream)
-                                            : run_up<F, A, CT, RC, UW, Way::SHIFTED>(c, stream);
+    const hipError_t st = up == Way::LDS    ? run_up<F, A, RC, kUpWaves, Way::LDS>(c, stream)
+                          : up == Way::ROWS ? run_up<F, A, RC, kUpWaves, Way::ROWS>(c, stream)
+                                            : run_up<F, A, RC, kUpWaves, Way::SHIFTED>(c, stream);
     if (st != hipSuccess)
         return st;
-    return down == Way::LDS    ? run_down<F, A, RC, DW, Way::LDS>(c, stream)
-           : down == Way::ROWS ? run_down<F, A, RC, DW, Way::ROWS>(c, stream)
-                               : run_down<F, A, RC, DW, Way::SHIFTED>(c, stream);
+    return down == Way::LDS    ? run_down<F, A, RC, kDownWaves, Way::LDS>(c, stream)
+           : down == Way::ROWS ? run_down<F, A, RC, kDownWaves, Way::ROWS>(c, stream)
+                               : run_down<F, A, RC, kDownWaves, Way::SHIFTED>(c, stream);
 }
 
 template <typename F, typename A>
 hipError_t launch_typed(const LayerCall& c, hipStream_t stream)
 {
     if (c.t == 1)
-        return run_both<F, A, 1, 0, 4, 8>(c, stream);
-    return c.t <= 16 ? run_both<F, A, 1, 1, 4, 8>(c, stream) : run_both<F, A, 1, 2, 4, 8>(c, stream);
+        return run_both<F, A, 0>(c, stream);
+    return c.t <= 16 ? run_both<F, A, 1>(c, stream) : run_both<F, A, 2>(c, stream);
 }
 
 int64_t plan_numbers(int64_t t, int64_t e, int64_t top)
