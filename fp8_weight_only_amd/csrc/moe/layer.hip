@@ -10,15 +10,22 @@
 // together, with up to 32 of its rows: an expert with more is read twice. The
 // first workgroup leaves the plan for the second launch.
 //
-// Second launch: a workgroup owns 16 output channels of every token. The active
-// experts' blocks of k, in one line, are split evenly over its waves; a wave adds
-// weights[t, j] times its part of an expert's sums to its own fp32 accumulators in
-// LDS, and the waves' accumulators are added in wave order. No slot's result goes
-// through memory, and no sum depends on the order of anything.
+// Second launch: a workgroup has 16 output channels of every token, or where there
+// are few channels a part of their steps. The active experts' blocks of k, in one
+// line, are split evenly over its waves (over all waves of the workgroups that share
+// the channels); a wave adds weights[t, j] times its part of an expert's sums to its
+// own fp32 accumulators in LDS, and the waves' accumulators are added in wave order.
+// Workgroups that share channels leave those fp32 sums in the workspace and the last
+// one adds them in their order. What goes through memory besides is h: no slot's down
+// product does, and no sum depends on the order of anything.
 //
 // Sums, scales, biases, the activation and the weighted sum are fp32; h is rounded
 // once to the activation type, as the matrix cores take it (half a step of it per
-// value), and out once.
+// value), and out once. With both roundings the error to the 64-bit result is 1.4
+// times that of rounding out alone (bf16 2.4e-3 against 1.7e-3 of the norm, fp16 3.0e-4
+// against 2.1e-4), without a second pass of the matrix cores over h's lower bits. In
+// fp16 an h above 65504 is infinite, as a tensor of that type between separate calls
+// would be; it stays in its token.
 #include <algorithm>
 
 #include <stdio.h>

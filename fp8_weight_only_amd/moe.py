@@ -622,8 +622,8 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, top_k: int, gate_up, down, 
 
     x: [t, hidden] bf16 / fp16. gate_up, down: (q, scale) pairs of weights [e, 2 inner, hidden] (gate's rows first)
     and [e, hidden, inner], both from ``quantize_experts`` or both from ``quantize_fp4``. Biases [e, 2 inner] and
-    [e, hidden] of x.dtype. Sums in fp32; silu(gate) * up and the result are rounded to x.dtype. For more tokens call
-    ``route``, ``linear_experts`` (``linear_experts_fp4``) and ``combine``. ``workspace``: of
+    [e, hidden] of x.dtype. Sums in fp32; silu(gate) * up and the result are rounded to x.dtype (in fp16 a silu(gate) * up
+    above 65504 makes its token's row infinite or NaN, as it would between separate calls). For more tokens call ``route``, ``linear_experts`` (``linear_experts_fp4``) and ``combine``. ``workspace``: of
     moe_layer_workspace_bytes, allocated when None."""
     if workspace is None:
         r = (_FAST or _fast()).moe_layer(x, logits, top_k, gate_up, down, gate_up_bias, down_bias, renormalize, out)

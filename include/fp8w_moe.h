@@ -213,7 +213,8 @@ typedef enum fp8w_weight_format {
  *   choice and weights[t, j] of fp8w_route(logits, dtype, t, e, top_k, renormalize);
  *   gate, up = the expert's rows 0 .. inner - 1 and inner .. 2 inner - 1 of q_gate_up
  *              on x[t] (and their bias);
- *   h        = gate / (1 + exp(-gate)) * up, rounded to act_dtype;
+ *   h        = gate / (1 + exp(-gate)) * up, rounded to act_dtype (above 65504 in FP16:
+ *              infinite, and with it the token's row, infinite or NaN);
  *   out[t]   = sum_j weights[t, j] * (the expert's q_down on h, and its bias),
  * sums, scales, biases and the activation in fp32, out rounded once to act_dtype
  * (BF16 or FP16). Places of the choice that are left over add nothing: a padding
