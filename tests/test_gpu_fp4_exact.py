@@ -81,7 +81,7 @@ def _layer(seed, fmt, t, e, top, hidden, inner, dtype):
     x = ex.whole((t, hidden), g, dtype, 1)
     # about eight terms of 1 or 2 to a gate or up product, around a gate of 70
     up, wu = _stack(fmt, e, 2 * inner, hidden, min(1.0, 12.0 / hidden), g)
-    down, wd = _stack(fmt, e, hidden, inner, 0.5, g)
+    down, wd = _stack(fmt, e, hidden, inner, min(0.5, (300.0 if top == 64 else 1000.0) / inner), g)
     ub, db = ex.whole((e, 2 * inner), g, dtype, 3), ex.whole((e, hidden), g, dtype, 60)
     ub[:, :inner] += 70
     order = torch.rand((t, e), generator=g, device=DEV).argsort(dim=1)
@@ -128,3 +128,36 @@ def test_layer_shared_steps(t, e, top, hidden, inner, fmt, dtype):
                                                   (40, 2, 1, 512, 2048), (5, 1, 1, 256, 8200)])
 def test_layer_sizes(t, e, top, hidden, inner, fmt):
     _layer(t, fmt, t, e, top, hidden, inner, BF)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "fp4"])
+@pytest.mark.parametrize("t,e,top,hidden,inner", [(2, 1, 1, 1 << 22, 24), (1, 1, 1, (1 << 22) - 1, 9), (2, 1, 1, 24, 1 << 22),
+                                                  (17, 1, 1, 9, (1 << 22) - 3), (64, 64, 64, 17, 32700), (64, 1024, 2, 40, 96)])
+def test_layer_largest_widths(t, e, top, hidden, inner, fmt):
+    """The longest rows of either launch, and the most values between them."""
+    _layer(t, fmt, t, e, top, hidden, inner, BF)
+
+
+LONG = [(1, 48, 1 << 22), (3, 40, (1 << 22) - 2), (3, 40, (1 << 22) + 2), (20, 40, (1 << 22) + 128), (2, 16, 5000001)]
+
+
+@pytest.mark.parametrize("m,n,k", LONG)
+def test_linear_longest_rows(m, n, k):
+    """Up to the stream's and the rings' longest rows, and past them."""
+    g = torch.Generator(device=DEV).manual_seed(k)
+    x = ex.whole((m, k), g, BF, 1)
+    (q, s), w = _stack("fp4", 1, n, k, 0.5, g)
+    ex.assert_bits(fw.linear_fp4(x, q[0], s[0]), ex.product(x, w[0], unit=1.0), f"{m} {n} {k}")
+
+
+@pytest.mark.parametrize("m,e,n,k", [(300, 1024, 64, 256), (300, 1024, 70, 101), (3000, 1024, 64, 256), (40, 2, 64, (1 << 22) + 2)])
+def test_experts_largest(m, e, n, k):
+    """The most experts, most of them empty; the longest rows."""
+    g = torch.Generator(device=DEV).manual_seed(m + k)
+    x = ex.whole((m, k), g, BF, 1)
+    (q, s), w = _stack("fp4", e, n, k, 0.5, g)
+    ids = torch.sort(torch.randint(0, e, (m,), generator=g, device=DEV)).values
+    offsets = torch.searchsorted(ids, torch.arange(e + 1, device=DEV)).int()
+    out = fw.linear_experts_fp4(x, q, s, offsets)
+    ref = torch.cat([ex.product(x[ids == i], w[i], unit=1.0) for i in torch.unique(ids).tolist()])
+    ex.assert_bits(out, ref, f"{m} {e} {n} {k}")
