@@ -39,9 +39,9 @@ __device__ __forceinline__ RowTile row_tile(const Fp4Call& c, int want)
 // every WK-th step of k; the sums of WK waves meet in LDS and are added in wave order.
 // A wave's loads run a step ahead, into the next tile's weights.
 //
-// One row, [14336, 4096]: 9.2 us, 3.4 TB/s, as a wave's eight steps leave start and drain uncovered
-// ([28672, 8192]: 29.7 us, 4.2 TB/s). 512 rows over 128 experts [4096, 1024]: 61 us, 3.8
-// TB/s, the address unit busy 68 %.
+// One row, [14336, 4096] from memory: 10.7 us, 2.9 TB/s, on 224 workgroups with one of a wave's eight
+// steps in flight (9.3 where the weights are in the memory-side cache); [28672, 8192]: 31 us, 4.0 TB/s.
+// 512 rows over 128 experts [4096, 1024]: 62 us, 3.7 TB/s, the address unit busy 67 %.
 template <typename A, int CT, int WK, int WC, Way WAY>
 __global__ __launch_bounds__(WK* WC* kWave) void fp4_stream_kernel(Fp4Call c, int TN, int cols)
 {
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(WK* WC* kWave) void fp4_stream_kernel(Fp4Call c, in
 // bytes per row then meets each bank twice, without it four times. Eight bytes are
 // 16 codes, for two v_mfma_f32_32x32x16 of eight k each; both lie in one scale's
 // block (a part of a stage is 32 k). Unaligned rows bind by latency, not by a unit: 333 tokens, 4 of
-// 60 experts [1030, 1001], 24 us with the address unit busy 28 %, the matrix cores 16 %; stages of 128
+// 60 experts [1030, 1001], 24 us with the address unit busy 29 %, the matrix cores 17 %; stages of 128
 // and 256 k, with fewer workgroups on a CU, took 25 to 38.
 template <typename A, int BN, int BM, int WN, int WM, int Q = 1>
 struct Fp4Tile {
@@ -520,7 +520,8 @@ __global__ __launch_bounds__(WN* WM* kWave) void fp4_ring_kernel(Fp4Call c, int 
 // Blocks of 32 weights, eight lanes a block, four weights a lane. The scale is
 // the power of two with amax / scale in [4, 8): 2^(floor(log2 amax) - 2), codes the
 // nearest e2m1 values, ties to the even code, beyond 6 the code of 6 (the OCP
-// formats' own conversion). Build time: not tuned.
+// formats' own conversion). Build time, not tuned: [14336, 4096] of fp32 76 us, of bf16 91 (its bytes 52 and
+// 29); a call takes 250 with the scales' copy to the host.
 constexpr int kQuantThreads = 256;
 
 template <typename T>
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_fp4_kernel(const T* __
     }
 }
 
-// Eight weights a thread.
+// Eight weights a thread; [14336, 4096] to fp32 139 us, its bytes 52: not tuned either.
 __global__ __launch_bounds__(kQuantThreads) void dequantize_fp4_kernel(const uint8_t* __restrict__ q,
                                                                        const uint8_t* __restrict__ scale, int64_t n,
                                                                        int64_t k, void* __restrict__ out, Act type)
@@ -636,9 +637,9 @@ enum class Fp4Kind { STREAM, TILE, RING };
 // A kernel's tile, and what its calls take: start us, and for every 64 k of a
 // workgroup's k, wait and for every workgroup on its CU each + rows_part (of 16 rows in use;
 // less of fewer) us. Fitted to sweeps over layers of [1024, 1024] to [28672, 8192] with 1 to
-// 4096 rows (a stream's own three: one row, [28672, 8192], {2, 1, 4} 29.7, {2, 2, 2} 30.6, {1, 4, 1}
-// 36.8; [14336, 4096]: 15.0, 10.8, 13.4; [8192, 4096]: 14.3, 9.6, 8.4). The plan with the lowest
-// modelled time was the fastest measured or within 3 % of it in 40 of 44 calls, 15 % off at worst.
+// 4096 rows, weights from memory (a stream's own three: one row, [28672, 8192], {2, 1, 4} 30.2, {2, 2, 2}
+// 30.5, {1, 4, 1} 37.0; [14336, 4096]: 15.0, 10.8, 13.4; [4096, 4096]: 13.9, 9.0, 5.9). The plan with the lowest
+// modelled time was the fastest measured or within 5 % of it in 42 of 44 calls, 21 % off at worst.
 struct Fp4Plan {
     Fp4Kind kind;
     int a, b, w;  // stream: CT, 16, WK; tile, ring: BN, BM, waves
@@ -731,8 +732,9 @@ Fp4Plan fp4_plan(const Fp4Shape& s, const void* x, const uint8_t* q, const uint8
     for (const Fp4Plan& p : kStreams)
         if ((rows <= 16 || aligned) && stream_fits(s, p))
             offer(p);
-    // Few rows to an expert: rings of 32 rows load and multiply mostly nothing (128 experts of
-    // [4096, 1024], four rows each: 91 us, the stream 62).
+    // Few rows to an expert: rings of 32 rows load and multiply mostly nothing, and are modelled too fast (128
+    // experts [4096, 1024], 4 and 16 rows each: 113 and 117 us, streams 75 and 104; 32 experts [1024, 2048], 4
+    // rows: 12.8, 11.8). Only at 16 rows of few experts is a ring faster (8 experts [4096, 4096]: 20, 25).
     const bool few = s.grouped && rows <= 16 && any;
     if (aligned && !few && s.k > 0 && s.k <= (1 << 22) && (!s.grouped || s.xr <= ((int64_t)1 << 30) / s.k)) {
         for (const Fp4Plan& p : kRings)
